@@ -282,6 +282,39 @@ rswa_status rswa_masked_forward_varlen(const void* Q, const void* K, const void*
                                        int n, int H, int d, rswa_dtype dtype, float scale, int flags,
                                        void* stream);
 
+/* The teacher-forced form over a pack that also leaves what its gradient
+ * needs: rswa_masked_forward_varlen plus
+ *   lse: device float32 [H][L], the natural log of each row's sum of
+ *     exponentials, log sum_j exp(scale q_i.k_j) over the visible keys.
+ * One sequence is a pack of one document.  O is bit for bit the same. */
+rswa_status rswa_masked_forward_lse(const void* Q, const void* K, const void* V, void* O, float* lse,
+                                    const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n, int H,
+                                    int d, rswa_dtype dtype, float scale, int flags, void* stream);
+
+/* Gradient of the teacher-forced form over a pack (one sequence: one
+ * document).  Per head, over the visible pairs of the mask above,
+ *   P_ij = exp(scale q_i.k_j - lse_i), delta_i = O_i.dO_i,
+ *   dS_ij = P_ij (dO_i.v_j - delta_i),
+ *   dV_j = sum_i P_ij dO_i, dQ_i = scale sum_j dS_ij k_j,
+ *   dK_j = scale sum_i dS_ij q_i.
+ *   dO, Q, K, V, O: device [L][H][d]; O and lse (float32 [H][L]) as
+ *     rswa_masked_forward_lse left them for the same arguments.
+ *   dQ, dK, dV: device [L][H][d], every row written; they and the workspace
+ *     overlap no other tensor of the call.
+ *   workspace: device memory, at least rswa_masked_backward_workspace_bytes
+ *     of the same arguments (a pure host function; 0 for invalid arguments);
+ *     its contents need no preparation and mean nothing afterwards.  Calls
+ *     that may run at the same time need workspaces of their own.
+ * Every gradient element is summed in one fixed order in float32: the same
+ * call gives the same bits.  Every argument is checked before anything is
+ * enqueued; the host arrays are read during the call only. */
+size_t rswa_masked_backward_workspace_bytes(const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n,
+                                            int H, int d, rswa_dtype dtype, int flags);
+rswa_status rswa_masked_backward(const void* dO, const void* Q, const void* K, const void* V, const void* O,
+                                 const float* lse, void* dQ, void* dK, void* dV, const int32_t* cu_seqlens,
+                                 const int32_t* ref_lens, int n_docs, int n, int H, int d, rswa_dtype dtype,
+                                 float scale, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
 /* The teacher-forced form of one sequence that also leaves a handle's cache
  * ready to decode: O as rswa_masked_forward_ex computes it with the handle's
  * window (its n; every output for a FULL-mode handle, i.e. plain causal
@@ -301,6 +334,56 @@ rswa_status rswa_masked_forward_varlen(const void* Q, const void* K, const void*
  * reported before anything is enqueued. */
 rswa_status rswa_masked_forward_fill(rswa_handle h, const void* Q, const void* K, const void* V, void* O,
                                      int L, int L_m, float scale, int flags);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  The attention takes q and k with their positions already
+ * encoded; this encodes them.  Pair i of a head, at position m (0-based),
+ * turns by the angle m * theta_i and is scaled by mscale; the elements from
+ * `dim` on pass through.  The gradient of a turn is the inverse turn.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  RSWA_ROTARY_PLAIN = 0,  /* theta_i = base^(-2i/dim) */
+  RSWA_ROTARY_LINEAR = 1, /* theta_i / factor (positions compressed by factor) */
+  RSWA_ROTARY_NTK = 2,    /* base * factor^(dim/(dim-2)): the slowest pair slowed by factor, the fastest kept */
+  RSWA_ROTARY_YARN = 3    /* pairs with more than 32 turns over original_length kept, below 1 turn slowed by
+                             factor, a linear ramp between; mscale = 0.1 ln(factor) + 1 */
+} rswa_rotary_scaling;
+
+/* A plan is plain host data filled by rswa_rotary_plan; copy it freely. */
+typedef struct {
+  int32_t d;             /* head dim, 64 or 128 */
+  int32_t dim;           /* rotary elements of a head, even, 2 .. d */
+  int32_t interleaved;   /* pairs (x_2i, x_2i+1); 0: (x_i, x_{i + dim/2}) */
+  float mscale;
+  uint64_t turn[64];     /* theta_i / 2 pi in units of 2^-64 of a turn */
+} rswa_rotary;
+
+/* Host only.  base > 1; factor >= 1 (ignored by PLAIN); original_length >= 1
+ * (YARN only). */
+rswa_status rswa_rotary_plan(rswa_rotary* plan, int d, int dim, int interleaved, double base,
+                             rswa_rotary_scaling scaling, double factor, int original_length);
+
+/* Turns queries and (H_k > 0) keys in one launch.
+ *   Q: device [rows][H][d], row r at r * q_stride elements (stride >= H*d, a
+ *     multiple of 16 bytes: a slice of a fused projection will do); Q_out
+ *     likewise; in place when Q_out == Q with equal strides, otherwise a
+ *     result overlaps no tensor of the call.  K, K_out the same with H_k heads
+ *     (ignored when H_k = 0).
+ *   positions: device int32[rows], any int32 values; NULL: row r is at
+ *     first + r, within [0, 2^31).
+ *   inverse: 1 turns back by the same angles (the gradient of the turn). */
+rswa_status rswa_rotary_apply(const rswa_rotary* plan, const void* Q, long long q_stride, int H, void* Q_out,
+                              long long q_out_stride, const void* K, long long k_stride, int H_k, void* K_out,
+                              long long k_out_stride, const int32_t* positions, int first, int rows,
+                              rswa_dtype dtype, int inverse, void* stream);
+
+/* The turn for a handle's next decode step: q, k [batch][H][d] of output T+1
+ * turn to position L_m[b] + T (0-based), read from the handle's device-side
+ * step counter, so a captured graph of this call followed by
+ * rswa_append_decode replays step after step.  q_out == q and k_out == k turn
+ * in place. */
+rswa_status rswa_rotary_step(rswa_handle h, const rswa_rotary* plan, const void* q, const void* k, void* q_out,
+                             void* k_out);
 
 /* ------------------------------------------------------------------------
  * Decode without allocation.  The pages have no counterpart to this call;

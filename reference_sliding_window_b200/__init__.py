@@ -10,6 +10,12 @@ raise; nothing is computed any other way.
     attn.load_reference(K_ref, V_ref, ref_lens)        # [B, H, L_m_cap, d]
     o = attn.append_decode(k, v, q)                    # [B, H, d] each
     O = masked_forward(Q, K, V, L_m=..., n=128)        # [L, H, d]
+
+Training: masked_attention (and masked_attention_varlen, over a pack of
+documents) is the differentiable call; masked_backward(_varlen) is its
+gradient by itself, from the O and lse of masked_forward(_varlen)(...,
+return_lse=True).  Positions: Rotary turns q and k, by itself (apply) or
+inside RSWA.append_decode, RSWA.prefill and masked_attention (rotary=...).
 """
 
 from __future__ import annotations
@@ -23,7 +29,9 @@ import torch
 from . import _native
 from ._native import MODE_FULL, MODE_RSWA, RSWAError, check
 
-__all__ = ["RSWA", "LayerStep", "append_decode_layers", "masked_forward", "masked_forward_varlen", "RSWAError", "MODE_RSWA", "MODE_FULL", "library_version"]
+__all__ = ["RSWA", "LayerStep", "append_decode_layers", "masked_forward", "masked_forward_varlen",
+           "masked_backward", "masked_backward_varlen", "masked_attention", "masked_attention_varlen",
+           "Rotary", "document_positions", "RSWAError", "MODE_RSWA", "MODE_FULL", "library_version"]
 
 _DT = {torch.float32: _native.F32, torch.bfloat16: _native.BF16}
 
@@ -171,11 +179,14 @@ class RSWA:
         check(_native.lib().rswa_load_reference_chunk(self._h, K.data_ptr(), V.data_ptr(), stride, r))
 
     def prefill(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, scale: float = 0.0,
-                out: Optional[torch.Tensor] = None, bidir_prefix: bool = False) -> torch.Tensor:
+                out: Optional[torch.Tensor] = None, bidir_prefix: bool = False,
+                rotary: Optional["Rotary"] = None) -> torch.Tensor:
         """Teacher-forced attention of one sequence (Q, K, V: [L, H, d]) with
         this handle's window, that also fills the cache as a reference load of
         rows [0, L_m) plus L - L_m appends would; decoding continues at output
-        L - L_m + 1.  Batch-1 handles only."""
+        L - L_m + 1.  Batch-1 handles only.
+        rotary: Q and K are turned to positions 0 .. L-1 first (into copies;
+        the cache holds turned keys)."""
         if Q.dim() != 3:
             raise ValueError("Q must be [L, H, d]")
         L = Q.shape[0]
@@ -184,6 +195,8 @@ class RSWA:
         O = torch.empty_like(Q) if out is None else out
         _check_tensor("out", O, (L, self.H, self.d), self.dtype, self.device)
         self._sync_stream()
+        if rotary is not None:
+            Q, K = rotary.apply(Q, K)
         check(_native.lib().rswa_masked_forward_fill(self._h, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
                                                       L, int(L_m), float(scale),
                                                       _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0))
@@ -203,11 +216,31 @@ class RSWA:
         check(self._lib.rswa_decode(self._h, q.data_ptr(), o.data_ptr(), float(scale)))
         return o
 
+    def rotate(self, rotary: "Rotary", q: torch.Tensor, k: torch.Tensor, out=None) -> tuple:
+        """q, k ([B, H, d]) of the next output turned to its position, L_m[b]
+        plus the outputs appended so far, read from the device-side step
+        counter (so it may be captured with the append_decode that follows).
+        out: a (q, k) pair, (q, k) itself for in place.  Returns the pair."""
+        self._vec("q", q)
+        self._vec("k", k)
+        qo, ko = (torch.empty_like(q), torch.empty_like(k)) if out is None else out
+        self._vec("out[0]", qo)
+        self._vec("out[1]", ko)
+        self._sync_stream()
+        check(self._lib.rswa_rotary_step(self._h, rotary._plan, q.data_ptr(), k.data_ptr(), qo.data_ptr(),
+                                         ko.data_ptr()))
+        return qo, ko
+
     def append_decode(self, k: torch.Tensor, v: torch.Tensor, q: torch.Tensor,
-                      out: Optional[torch.Tensor] = None, scale: float = 0.0) -> torch.Tensor:
+                      out: Optional[torch.Tensor] = None, scale: float = 0.0,
+                      rotary: Optional["Rotary"] = None) -> torch.Tensor:
+        """Appends k, v and attends with q.  rotary: q and k are turned to the
+        step's position first (rotate, into copies)."""
         self._vec("k", k)
         self._vec("v", v)
         self._vec("q", q)
+        if rotary is not None:
+            q, k = self.rotate(rotary, q, k)
         o = torch.empty_like(q) if out is None else out
         self._vec("out", o)
         self._sync_stream()
@@ -326,14 +359,46 @@ class LayerStep:
             self._launch()
 
 
-def masked_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, n: int,
-                   scale: float = 0.0, out: Optional[torch.Tensor] = None,
-                   bidir_prefix: bool = False) -> torch.Tensor:
-    """Teacher-forced R-SWA attention.  Q, K, V, out: [L, H, d] on a B200.
-    L_m = 0: no reference segment (the plain sliding window of n).
-    bidir_prefix: prefix queries see every reference key (default: causal)."""
+def _pack_args(Q: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[int]):
+    """Checks Q and the documents; -> (L, H, d, cu, refs) with the host arrays as ctypes."""
     if Q.dim() != 3:
         raise ValueError("Q must be [L, H, d]")
+    L, H, d = Q.shape
+    if Q.dtype not in _DT:
+        raise ValueError(f"dtype {Q.dtype} not supported")
+    n_docs = len(ref_lens)
+    if len(cu_seqlens) != n_docs + 1 or int(cu_seqlens[-1]) != L:
+        raise ValueError("cu_seqlens must have len(ref_lens) + 1 entries ending at L")
+    return L, H, d, (C.c_int32 * (n_docs + 1))(*map(int, cu_seqlens)), (C.c_int32 * max(n_docs, 1))(*map(int, ref_lens))
+
+
+def _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, out, bidir_prefix):
+    L, H, d, cu, refs = _pack_args(Q, cu_seqlens, ref_lens)
+    for name, t in (("K", K), ("V", V), ("Q", Q)):
+        _check_tensor(name, t, (L, H, d), Q.dtype, Q.device)
+    O = torch.empty_like(Q) if out is None else out
+    _check_tensor("out", O, (L, H, d), Q.dtype, Q.device)
+    lse = torch.empty((H, L), dtype=torch.float32, device=Q.device)
+    with torch.cuda.device(Q.device):
+        check(_native.lib().rswa_masked_forward_lse(
+            Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), cu, refs, len(ref_lens), int(n),
+            H, d, _DT[Q.dtype], float(scale), _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0,
+            _stream_ptr(Q.device)))
+    return O, lse
+
+
+def masked_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, n: int,
+                   scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                   bidir_prefix: bool = False, return_lse: bool = False):
+    """Teacher-forced R-SWA attention.  Q, K, V, out: [L, H, d] on a B200.
+    L_m = 0: no reference segment (the plain sliding window of n).
+    bidir_prefix: prefix queries see every reference key (default: causal).
+    return_lse: returns (O, lse) with lse float32 [H, L], the natural log of
+    each row's sum of exponentials, as masked_backward takes it."""
+    if Q.dim() != 3:
+        raise ValueError("Q must be [L, H, d]")
+    if return_lse:
+        return _forward_lse(Q, K, V, (0, Q.shape[0]), (L_m,), n, scale, out, bidir_prefix)
     L, H, d = Q.shape
     if Q.dtype not in _DT:
         raise ValueError(f"dtype {Q.dtype} not supported")
@@ -352,11 +417,14 @@ def masked_forward(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, 
 
 def masked_forward_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqlens: Sequence[int],
                           ref_lens: Sequence[int], n: int, scale: float = 0.0,
-                          out: Optional[torch.Tensor] = None, bidir_prefix: bool = False) -> torch.Tensor:
+                          out: Optional[torch.Tensor] = None, bidir_prefix: bool = False,
+                          return_lse: bool = False):
     """Teacher-forced R-SWA attention over a pack of documents.  Q, K, V, out:
     [L, H, d] on a B200, L = cu_seqlens[-1]; document i holds rows
     cu_seqlens[i] .. cu_seqlens[i+1]-1 with ref_lens[i] reference rows and
-    sees only its own keys."""
+    sees only its own keys.  return_lse: as masked_forward."""
+    if return_lse:
+        return _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, out, bidir_prefix)
     if Q.dim() != 3:
         raise ValueError("Q must be [L, H, d]")
     L, H, d = Q.shape
@@ -377,3 +445,175 @@ def masked_forward_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_
             _DT[Q.dtype], float(scale), _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0,
             _stream_ptr(Q.device)))
     return O
+
+
+def masked_backward(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+                    lse: torch.Tensor, L_m: int, n: int, scale: float = 0.0, out=None,
+                    bidir_prefix: bool = False) -> tuple:
+    """Gradient of masked_forward: (dQ, dK, dV) for the gradient dO of its
+    output, from its inputs and the (O, lse) it returned with return_lse=True
+    (the same L_m, n, scale and bidir_prefix).  All [L, H, d], lse [H, L]
+    float32.  out: three tensors to write, apart from every input.  The same
+    call gives the same bits."""
+    if Q.dim() != 3:
+        raise ValueError("Q must be [L, H, d]")
+    return masked_backward_varlen(dO, Q, K, V, O, lse, (0, Q.shape[0]), (L_m,), n, scale, out, bidir_prefix)
+
+
+def masked_backward_varlen(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor,
+                           lse: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[int], n: int,
+                           scale: float = 0.0, out=None, bidir_prefix: bool = False) -> tuple:
+    """Gradient of masked_forward_varlen, as masked_backward: (dQ, dK, dV)."""
+    L, H, d, cu, refs = _pack_args(Q, cu_seqlens, ref_lens)
+    grads = tuple(torch.empty_like(Q) for _ in range(3)) if out is None else tuple(out)
+    if len(grads) != 3:
+        raise ValueError("out must be three tensors")
+    for name, t in (("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O),
+                    ("out[0]", grads[0]), ("out[1]", grads[1]), ("out[2]", grads[2])):
+        _check_tensor(name, t, (L, H, d), Q.dtype, Q.device)
+    _check_tensor("lse", lse, (H, L), torch.float32, Q.device)
+    lib = _native.lib()
+    flags = _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0
+    ws_bytes = lib.rswa_masked_backward_workspace_bytes(cu, refs, len(ref_lens), int(n), H, d, _DT[Q.dtype], flags)
+    # 0 bytes: arguments that the call itself reports
+    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=Q.device)
+    with torch.cuda.device(Q.device):
+        check(lib.rswa_masked_backward(
+            dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(),
+            grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), cu, refs, len(ref_lens), int(n), H, d,
+            _DT[Q.dtype], float(scale), flags, ws.data_ptr(), ws_bytes, _stream_ptr(Q.device)))
+    return grads
+
+
+class Rotary:
+    """A plan of rotary positions for heads of d (64 or 128) elements.
+
+    rotary_dim: the elements of a head that turn (even; default all of them).
+    interleaved: pairs (x_2i, x_2i+1); default (x_i, x_{i + rotary_dim/2}).
+    scaling, for contexts longer than trained: None, "linear" (positions
+    compressed by factor), "ntk" (a larger base) or "yarn" (by parts, over the
+    original_length that the model was trained on, with its magnitude
+    0.1 ln(factor) + 1)."""
+
+    _SCALINGS = {None: _native.ROTARY_PLAIN, "linear": _native.ROTARY_LINEAR, "ntk": _native.ROTARY_NTK,
+                 "yarn": _native.ROTARY_YARN}
+
+    def __init__(self, d: int, rotary_dim: Optional[int] = None, base: float = 10000.0, interleaved: bool = False,
+                 scaling: Optional[str] = None, factor: float = 1.0, original_length: int = 0):
+        if scaling not in self._SCALINGS:
+            raise ValueError(f"scaling {scaling!r} not one of None, 'linear', 'ntk', 'yarn'")
+        self.d, self.rotary_dim = int(d), int(d if rotary_dim is None else rotary_dim)
+        self.interleaved = bool(interleaved)
+        self._plan = _native.RotaryPlan()
+        check(_native.lib().rswa_rotary_plan(C.byref(self._plan), self.d, self.rotary_dim, int(self.interleaved),
+                                             float(base), self._SCALINGS[scaling], float(factor),
+                                             int(original_length)))
+        self.mscale = self._plan.mscale
+
+    def _stride(self, name: str, t: torch.Tensor, rows: int, like: torch.Tensor) -> int:
+        """Checks t ([rows, heads, d] with contiguous heads, a slice of wider
+        rows or not) and returns its row stride in elements."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != self.d:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, heads, {self.d}]")
+        if t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
+        heads = t.shape[1]
+        s = t.stride()
+        if s[2] != 1 or (heads > 1 and s[1] != self.d):
+            raise ValueError(f"{name} must have contiguous heads")
+        return s[0] if rows > 1 else heads * self.d
+
+    def apply(self, Q: torch.Tensor, K: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              first: int = 0, inverse: bool = False, out=None):
+        """Q (and K) [rows, heads, d] turned to their positions, in one launch.
+
+        positions: int32 [rows] on the device; None: first, first + 1, ...
+        inverse: turned back by the same angles (the gradient).
+        Rows may be slices of wider ones (a fused projection); out (Q's
+        result, or the pair) may be such slices too, or the inputs
+        themselves.  Returns Q's result, or the pair."""
+        if not isinstance(Q, torch.Tensor):
+            raise TypeError("Q must be a torch.Tensor")
+        if Q.device.type != "cuda":
+            raise ValueError(f"Q is on {Q.device}, expected a CUDA device")
+        if Q.dtype not in _DT:
+            raise ValueError(f"dtype {Q.dtype} not supported")
+        rows = Q.shape[0] if Q.dim() == 3 else 0
+        ins = (Q,) if K is None else (Q, K)
+        if out is None:
+            outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins)
+        else:
+            outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(outs) != len(ins):
+            raise ValueError("out must hold one tensor for Q and one for K")
+        args = []
+        for name, t, o in zip(("Q", "K"), ins, outs):
+            sx = self._stride(name, t, rows, Q)
+            so = self._stride("out of " + name, o, rows, Q)
+            if o.shape != t.shape:
+                raise ValueError(f"out of {name} has shape {tuple(o.shape)}, expected {tuple(t.shape)}")
+            args += [t.data_ptr(), sx, t.shape[1], o.data_ptr(), so]
+        if K is None:
+            args += [None, 0, 0, None, 0]
+        pos = None
+        if positions is not None:
+            _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
+            pos = positions.data_ptr()
+        with torch.cuda.device(Q.device):
+            check(_native.lib().rswa_rotary_apply(self._plan, *args, pos, int(first), rows, _DT[Q.dtype],
+                                                  int(bool(inverse)), _stream_ptr(Q.device)))
+        return outs[0] if K is None else outs
+
+
+def document_positions(cu_seqlens: Sequence[int], device=None) -> torch.Tensor:
+    """int32 positions of a pack's rows, each document from 0 on, on the
+    device (copied from the host: not inside a graph capture)."""
+    cu = np.asarray([int(x) for x in cu_seqlens], dtype=np.int64)
+    if cu.size < 2 or cu[0] != 0 or (np.diff(cu) < 1).any():
+        raise ValueError("cu_seqlens must start at 0 and increase")
+    pos = np.arange(cu[-1], dtype=np.int64) - np.repeat(cu[:-1], np.diff(cu))
+    return torch.from_numpy(pos.astype(np.int32)).to(torch.device("cuda") if device is None else device)
+
+
+class _MaskedAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, V, cu_seqlens, ref_lens, n, scale, bidir_prefix, rotary, positions):
+        if rotary is not None:
+            Q, K = rotary.apply(Q, K, positions=positions)
+        O, lse = _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, None, bidir_prefix)
+        ctx.save_for_backward(Q, K, V, O, lse, positions)
+        ctx.args = (cu_seqlens, ref_lens, n, scale, None, bidir_prefix)
+        ctx.rotary = rotary
+        return O
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, lse, positions = ctx.saved_tensors
+        dQ, dK, dV = masked_backward_varlen(dO.contiguous(), Q, K, V, O, lse, *ctx.args)
+        if ctx.rotary is not None:
+            ctx.rotary.apply(dQ, dK, positions=positions, inverse=True, out=(dQ, dK))
+        return (dQ, dK, dV) + (None,) * 7
+
+
+def masked_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, n: int, scale: float = 0.0,
+                     bidir_prefix: bool = False, rotary: Optional[Rotary] = None,
+                     positions: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """masked_forward as a differentiable function of Q, K and V (once
+    differentiable).  rotary: Q and K are turned first, to positions (int32
+    [L] on the device; None: 0 .. L-1), and their gradients turned back."""
+    return _MaskedAttention.apply(Q, K, V, (0, Q.shape[0]), (int(L_m),), n, scale, bidir_prefix, rotary, positions)
+
+
+def masked_attention_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqlens: Sequence[int],
+                            ref_lens: Sequence[int], n: int, scale: float = 0.0, bidir_prefix: bool = False,
+                            rotary: Optional[Rotary] = None, positions: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """masked_forward_varlen as a differentiable function, as
+    masked_attention.  rotary without positions: document_positions of the
+    pack (pass them to reuse them over a model's layers or to capture)."""
+    if rotary is not None and positions is None:
+        positions = document_positions(cu_seqlens, Q.device)
+    cu, refs = tuple(int(x) for x in cu_seqlens), tuple(int(x) for x in ref_lens)
+    return _MaskedAttention.apply(Q, K, V, cu, refs, n, scale, bidir_prefix, rotary, positions)

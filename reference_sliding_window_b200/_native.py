@@ -18,8 +18,18 @@ STATUS_NAMES = ["RSWA_OK", "RSWA_ERR_ARG", "RSWA_ERR_STATE", "RSWA_ERR_CAPACITY"
 F32, BF16 = 0, 1
 MODE_RSWA, MODE_FULL = 0, 1
 FLAG_BIDIR_PREFIX = 1
+# rswa_rotary_scaling
+ROTARY_PLAIN, ROTARY_LINEAR, ROTARY_NTK, ROTARY_YARN = range(4)
+
+
+class RotaryPlan(C.Structure):
+    """rswa_rotary."""
+    _fields_ = [("d", C.c_int32), ("dim", C.c_int32), ("interleaved", C.c_int32), ("mscale", C.c_float),
+                ("turn", C.c_uint64 * 64)]
+
 
 _i, _f, _p, _sz = C.c_int, C.c_float, C.c_void_p, C.c_size_t
+_d, _ll, _pi32 = C.c_double, C.c_longlong, C.POINTER(C.c_int32)
 _PROTOS = {
     "rswa_cache_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
     "rswa_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
@@ -44,6 +54,14 @@ _PROTOS = {
     "rswa_masked_forward_fill": (_i, [_p, _p, _p, _p, _p, _i, _i, _f, _i]),
     "rswa_masked_forward_varlen": (_i, [_p, _p, _p, _p, C.POINTER(C.c_int32), C.POINTER(C.c_int32), _i, _i,
                                        _i, _i, _i, _f, _i, _p]),
+    "rswa_masked_forward_lse": (_i, [_p, _p, _p, _p, _p, _pi32, _pi32, _i, _i, _i, _i, _i, _f, _i, _p]),
+    "rswa_masked_backward_workspace_bytes": (_sz, [_pi32, _pi32, _i, _i, _i, _i, _i, _i]),
+    "rswa_masked_backward": (_i, [_p, _p, _p, _p, _p, _p, _p, _p, _p, _pi32, _pi32, _i, _i, _i, _i, _i, _f, _i,
+                                  _p, _sz, _p]),
+    "rswa_rotary_plan": (_i, [C.POINTER(RotaryPlan), _i, _i, _i, _d, _i, _d, _i]),
+    "rswa_rotary_apply": (_i, [C.POINTER(RotaryPlan), _p, _ll, _i, _p, _ll, _p, _ll, _i, _p, _ll, _p, _i, _i, _i,
+                               _i, _p]),
+    "rswa_rotary_step": (_i, [_p, C.POINTER(RotaryPlan), _p, _p, _p, _p]),
     "rswa_decode_noalloc": (_i, [_p, _p, _i, C.POINTER(C.c_int32), _p, _p, _i, _i, _i, _i, _f, _p]),
     "rswa_decode_noalloc_check": (_i, [_p]),
     "rswa_plan_decode": (_i, [_i, _i, C.POINTER(C.c_int32), _i, _i, _i, _i, C.POINTER(C.c_int32), _i,

@@ -17,8 +17,10 @@
 #include <string>
 #include <vector>
 
+#include "backward.h"
 #include "cache_copy.h"
 #include "internal.h"
+#include "rotary.h"
 #include "rswa.h"
 
 using namespace rswa;
@@ -817,9 +819,19 @@ extern "C" rswa_status rswa_masked_forward(const void* Q, const void* K, const v
   return rswa_masked_forward_ex(Q, K, V, O, L, L_m, n, H, d, dtype, scale, 0, stream);
 }
 
+static rswa_status masked_forward_one(const void* Q, const void* K, const void* V, void* O, int L, int L_m, int n,
+                                      int H, int d, rswa_dtype dtype, float scale, int flags, float* lse,
+                                      int lse_stride, void* stream);
+
 extern "C" rswa_status rswa_masked_forward_ex(const void* Q, const void* K, const void* V, void* O, int L,
                                               int L_m, int n, int H, int d, rswa_dtype dtype, float scale,
                                               int flags, void* stream) {
+  return masked_forward_one(Q, K, V, O, L, L_m, n, H, d, dtype, scale, flags, nullptr, 0, stream);
+}
+
+static rswa_status masked_forward_one(const void* Q, const void* K, const void* V, void* O, int L, int L_m, int n,
+                                      int H, int d, rswa_dtype dtype, float scale, int flags, float* lse,
+                                      int lse_stride, void* stream) {
   if (!Q || !K || !V || !O) return fail(RSWA_ERR_ARG, "rswa_masked_forward: null tensor");
   if (flags & ~(int)RSWA_FLAG_BIDIR_PREFIX) return fail(RSWA_ERR_ARG, "rswa_masked_forward: unknown flags %d", flags);
   if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O))
@@ -852,6 +864,8 @@ extern "C" rswa_status rswa_masked_forward_ex(const void* Q, const void* K, cons
   const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
   p.scale_log2 = sc * 1.4426950408889634f;
   p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
+  p.lse = lse;
+  p.lse_stride = lse_stride;
   p.timing = g_timing;
   const int32_t cu[2] = {0, L}, refs[1] = {L_m};
   p.cu = cu;
@@ -868,10 +882,27 @@ extern "C" rswa_status rswa_masked_forward_ex(const void* Q, const void* K, cons
   return RSWA_OK;
 }
 
+static rswa_status masked_forward_pack(const void* Q, const void* K, const void* V, void* O, float* lse,
+                                       const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n, int H,
+                                       int d, rswa_dtype dtype, float scale, int flags, void* stream);
+
 extern "C" rswa_status rswa_masked_forward_varlen(const void* Q, const void* K, const void* V, void* O,
                                                   const int32_t* cu_seqlens, const int32_t* ref_lens,
                                                   int n_docs, int n, int H, int d, rswa_dtype dtype,
                                                   float scale, int flags, void* stream) {
+  return masked_forward_pack(Q, K, V, O, nullptr, cu_seqlens, ref_lens, n_docs, n, H, d, dtype, scale, flags, stream);
+}
+
+extern "C" rswa_status rswa_masked_forward_lse(const void* Q, const void* K, const void* V, void* O, float* lse,
+                                               const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n,
+                                               int H, int d, rswa_dtype dtype, float scale, int flags, void* stream) {
+  if (!lse || !aligned16(lse)) return fail(RSWA_ERR_ARG, "rswa_masked_forward_lse: lse must be 16-byte aligned");
+  return masked_forward_pack(Q, K, V, O, lse, cu_seqlens, ref_lens, n_docs, n, H, d, dtype, scale, flags, stream);
+}
+
+static rswa_status masked_forward_pack(const void* Q, const void* K, const void* V, void* O, float* lse,
+                                       const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n, int H,
+                                       int d, rswa_dtype dtype, float scale, int flags, void* stream) {
   if (!Q || !K || !V || !O || !cu_seqlens || !ref_lens)
     return fail(RSWA_ERR_ARG, "rswa_masked_forward_varlen: null argument");
   if (n_docs < 1) return fail(RSWA_ERR_ARG, "rswa_masked_forward_varlen: n_docs=%d", n_docs);
@@ -917,6 +948,8 @@ extern "C" rswa_status rswa_masked_forward_varlen(const void* Q, const void* K, 
     const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
     p.scale_log2 = sc * 1.4426950408889634f;
     p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
+    p.lse = lse;
+    p.lse_stride = cu_seqlens[n_docs];
     p.timing = g_timing;
     p.cu = cu_seqlens;
     p.refs = ref_lens;
@@ -930,10 +963,10 @@ extern "C" rswa_status rswa_masked_forward_varlen(const void* Q, const void* K, 
   const size_t row_bytes = (size_t)H * d * elem_size(dtype);
   for (int i = 0; i < n_docs; ++i) {
     const size_t off = (size_t)cu_seqlens[i] * row_bytes;
-    rswa_status st = rswa_masked_forward_ex(static_cast<const uint8_t*>(Q) + off, static_cast<const uint8_t*>(K) + off,
-                                            static_cast<const uint8_t*>(V) + off, static_cast<uint8_t*>(O) + off,
-                                            cu_seqlens[i + 1] - cu_seqlens[i], ref_lens[i], n, H, d, dtype,
-                                            scale, flags, stream);
+    rswa_status st = masked_forward_one(static_cast<const uint8_t*>(Q) + off, static_cast<const uint8_t*>(K) + off,
+                                        static_cast<const uint8_t*>(V) + off, static_cast<uint8_t*>(O) + off,
+                                        cu_seqlens[i + 1] - cu_seqlens[i], ref_lens[i], n, H, d, dtype, scale, flags,
+                                        lse ? lse + cu_seqlens[i] : nullptr, cu_seqlens[n_docs], stream);
     if (st != RSWA_OK) return st;
   }
   return RSWA_OK;
@@ -984,6 +1017,8 @@ extern "C" rswa_status rswa_masked_forward_fill(rswa_handle h, const void* Q, co
     const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)h->d);
     p.scale_log2 = sc * 1.4426950408889634f;
     p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
+    p.lse = nullptr;
+    p.lse_stride = 0;
     p.timing = g_timing;
     const int32_t cu[2] = {0, L}, refs[1] = {L_m};
     p.cu = cu;
@@ -1019,6 +1054,260 @@ extern "C" rswa_status rswa_masked_forward_fill(rswa_handle h, const void* Q, co
     RSWA_CUDA(launch_load_packed(p, L_m + W, h->stream), "load_packed kernel");
   }
   h->loaded = true;
+  return RSWA_OK;
+}
+
+// ------------------------------------------- gradient of the masked forward
+
+// Checks a pack's documents; *rows receives the pack's length.
+static rswa_status check_documents(const char* who, const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs) {
+  if (!cu_seqlens || !ref_lens) return fail(RSWA_ERR_ARG, "%s: null cu_seqlens or ref_lens", who);
+  if (n_docs < 1) return fail(RSWA_ERR_ARG, "%s: n_docs=%d", who, n_docs);
+  if (cu_seqlens[0] != 0) return fail(RSWA_ERR_ARG, "%s: cu_seqlens[0] must be 0", who);
+  for (int i = 0; i < n_docs; ++i) {
+    const long long len = (long long)cu_seqlens[i + 1] - cu_seqlens[i];
+    if (len < 1) return fail(RSWA_ERR_ARG, "%s: document %d has %lld rows", who, i, len);
+    if (ref_lens[i] < 0 || ref_lens[i] > len)
+      return fail(RSWA_ERR_ARG, "%s: ref_lens[%d]=%d outside [0, %lld]", who, i, ref_lens[i], len);
+  }
+  return RSWA_OK;
+}
+
+static rswa_status check_backward(const char* who, const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n,
+                                  int H, int d, rswa_dtype dtype, int flags) {
+  if (rswa_status st = check_documents(who, cu_seqlens, ref_lens, n_docs)) return st;
+  if (flags & ~(int)RSWA_FLAG_BIDIR_PREFIX) return fail(RSWA_ERR_ARG, "%s: unknown flags %d", who, flags);
+  if (!dtype_ok(dtype)) return fail(RSWA_ERR_UNSUPPORTED, "%s: unknown dtype", who);
+  if (d != 64 && d != 128) return fail(RSWA_ERR_UNSUPPORTED, "%s: head dim %d", who, d);
+  if (H < 1 || n < 1) return fail(RSWA_ERR_ARG, "%s: H=%d n=%d", who, H, n);
+  if ((long long)cu_seqlens[n_docs] * H >= (1ll << 31) / d) return fail(RSWA_ERR_ARG, "%s: tensor too large", who);
+  return RSWA_OK;
+}
+
+extern "C" size_t rswa_masked_backward_workspace_bytes(const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs,
+                                                       int n, int H, int d, rswa_dtype dtype, int flags) {
+  if (check_backward("rswa_masked_backward_workspace_bytes", cu_seqlens, ref_lens, n_docs, n, H, d, dtype, flags))
+    return 0;
+  try {
+    return backward_workspace_bytes(cu_seqlens, ref_lens, n_docs, n, H, d, dtype == RSWA_BF16 ? kBF16 : kF32,
+                                    (flags & RSWA_FLAG_BIDIR_PREFIX) != 0);
+  } catch (...) {
+    fail(RSWA_ERR_CAPACITY, "rswa_masked_backward_workspace_bytes: out of host memory");
+    return 0;
+  }
+}
+
+extern "C" rswa_status rswa_masked_backward(const void* dO, const void* Q, const void* K, const void* V, const void* O,
+                                            const float* lse, void* dQ, void* dK, void* dV, const int32_t* cu_seqlens,
+                                            const int32_t* ref_lens, int n_docs, int n, int H, int d, rswa_dtype dtype,
+                                            float scale, int flags, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  static const char* who = "rswa_masked_backward";
+  const void* in[6] = {dO, Q, K, V, O, lse};
+  const void* out[4] = {dQ, dK, dV, workspace};
+  for (const void* t : in)
+    if (!t || !aligned16(t)) return fail(RSWA_ERR_ARG, "%s: tensors must be non-null and 16-byte aligned", who);
+  for (const void* t : out)
+    if (!t || !aligned16(t))
+      return fail(RSWA_ERR_ARG, "%s: gradients and workspace must be non-null and 16-byte aligned", who);
+  if (rswa_status st = check_backward(who, cu_seqlens, ref_lens, n_docs, n, H, d, dtype, flags)) return st;
+  if (!(scale == scale) || isinf(scale)) return fail(RSWA_ERR_ARG, "%s: scale not finite", who);
+  const int L = cu_seqlens[n_docs];
+  const size_t bytes = (size_t)L * H * d * elem_size(dtype), lse_bytes = (size_t)L * H * sizeof(float);
+  // Items read whole input tensors while others write gradients.
+  for (int i = 0; i < 4; ++i) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out[i]), a_end = a + (i < 3 ? bytes : workspace_bytes);
+    for (int j = 0; j < 6 + i; ++j) {
+      const void* t = j < 6 ? in[j] : out[j - 6];
+      const uintptr_t b = reinterpret_cast<uintptr_t>(t), b_end = b + (j == 5 ? lse_bytes : bytes);
+      if (a < b_end && b < a_end)
+        return fail(RSWA_ERR_ARG, "%s: a gradient or the workspace overlaps another tensor", who);
+    }
+  }
+  try {
+    const int elem = dtype == RSWA_BF16 ? kBF16 : kF32;
+    const bool bidir = (flags & RSWA_FLAG_BIDIR_PREFIX) != 0;
+    const size_t need = backward_workspace_bytes(cu_seqlens, ref_lens, n_docs, n, H, d, elem, bidir);
+    if (workspace_bytes < need)
+      return fail(RSWA_ERR_ARG, "%s: workspace of %zu bytes, %zu needed", who, workspace_bytes, need);
+    int dev = 0, major = 0, minor = 0;
+    RSWA_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
+    RSWA_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev), "device attribute");
+    RSWA_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev), "device attribute");
+    if (major != 10 || minor != 0)
+      return fail(RSWA_ERR_UNSUPPORTED, "%s: device is sm_%d%d; built for sm_100a", who, major, minor);
+    BackwardParams p = {};
+    p.dO = dO;
+    p.Q = Q;
+    p.K = K;
+    p.V = V;
+    p.O = O;
+    p.lse = lse;
+    p.dQ = dQ;
+    p.dK = dK;
+    p.dV = dV;
+    p.L = L;
+    p.n = n;
+    p.H = H;
+    p.D = d;
+    p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
+    p.bidir = bidir ? 1 : 0;
+    p.cu = cu_seqlens;
+    p.refs = ref_lens;
+    p.n_docs = n_docs;
+    RSWA_CUDA(launch_backward(p, elem, workspace, static_cast<cudaStream_t>(stream)), "masked backward kernels");
+  } catch (...) {
+    return fail(RSWA_ERR_CAPACITY, "%s: out of host memory", who);
+  }
+  return RSWA_OK;
+}
+
+// --------------------------------------------------------- rotary positions
+
+extern "C" rswa_status rswa_rotary_plan(rswa_rotary* plan, int d, int dim, int interleaved, double base,
+                                        rswa_rotary_scaling scaling, double factor, int original_length) {
+  static const char* who = "rswa_rotary_plan";
+  if (!plan) return fail(RSWA_ERR_ARG, "%s: null plan", who);
+  if (d != 64 && d != 128) return fail(RSWA_ERR_UNSUPPORTED, "%s: head dim %d", who, d);
+  if (dim < 2 || dim > d || dim % 2) return fail(RSWA_ERR_ARG, "%s: rotary dim %d outside 2, 4 .. %d", who, dim, d);
+  if (!(base > 1.0) || isinf(base)) return fail(RSWA_ERR_ARG, "%s: base must be finite and above 1", who);
+  if (scaling < RSWA_ROTARY_PLAIN || scaling > RSWA_ROTARY_YARN)
+    return fail(RSWA_ERR_ARG, "%s: unknown scaling %d", who, (int)scaling);
+  if (scaling != RSWA_ROTARY_PLAIN && (!(factor >= 1.0) || isinf(factor)))
+    return fail(RSWA_ERR_ARG, "%s: factor must be finite and at least 1", who);
+  if (scaling == RSWA_ROTARY_NTK && dim < 4) return fail(RSWA_ERR_ARG, "%s: NTK scaling needs a rotary dim of 4", who);
+  if (scaling == RSWA_ROTARY_YARN && original_length < 1)
+    return fail(RSWA_ERR_ARG, "%s: original_length=%d", who, original_length);
+  const double two_pi = 6.283185307179586476925;
+  if (scaling == RSWA_ROTARY_NTK) base *= pow(factor, (double)dim / (dim - 2));
+  if (isinf(base)) return fail(RSWA_ERR_ARG, "%s: base too large", who);
+  // YaRN: pairs that turn more than 32 times over the original context are
+  // kept, those below one turn are slowed by factor, with a ramp between.
+  double lo = 0, hi = 0;
+  if (scaling == RSWA_ROTARY_YARN) {
+    const double per = dim / (2.0 * log(base));
+    lo = std::max(floor(per * log(original_length / (two_pi * 32.0))), 0.0);
+    hi = std::min(ceil(per * log(original_length / two_pi)), dim - 1.0);
+  }
+  rswa_rotary r = {};
+  r.d = d;
+  r.dim = dim;
+  r.interleaved = interleaved ? 1 : 0;
+  r.mscale = scaling == RSWA_ROTARY_YARN && factor > 1.0 ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+  for (int i = 0; i < dim / 2; ++i) {
+    double theta = pow(base, -2.0 * i / dim);
+    if (scaling == RSWA_ROTARY_LINEAR) theta /= factor;
+    if (scaling == RSWA_ROTARY_YARN) {
+      const double w = std::min(std::max((i - lo) / std::max(hi - lo, 1e-3), 0.0), 1.0);
+      theta = theta * (1.0 - w) + theta / factor * w;
+    }
+    // theta <= 1 radian: a fraction of a turn below 2^-2, in units of 2^-64
+    r.turn[i] = (uint64_t)ldexp(theta / two_pi, 64);
+  }
+  *plan = r;
+  return RSWA_OK;
+}
+
+static rswa_status check_rotary(const char* who, const rswa_rotary* plan) {
+  if (!plan) return fail(RSWA_ERR_ARG, "%s: null plan", who);
+  if ((plan->d != 64 && plan->d != 128) || plan->dim < 2 || plan->dim > plan->d || plan->dim % 2)
+    return fail(RSWA_ERR_ARG, "%s: plan not made by rswa_rotary_plan", who);
+  return RSWA_OK;
+}
+
+// One tensor of a call: [rows][H][d] with rows `stride` elements apart.
+static rswa_status check_rotary_tensor(const char* who, const char* name, const void* x, const void* y, long long sx,
+                                       long long sy, int H, int d, rswa_dtype dtype) {
+  if (!x || !y) return fail(RSWA_ERR_ARG, "%s: null %s", who, name);
+  if (!aligned16(x) || !aligned16(y)) return fail(RSWA_ERR_ARG, "%s: %s must be 16-byte aligned", who, name);
+  const long long vec = 16 / elem_size(dtype);
+  for (long long s : {sx, sy})
+    if (s < (long long)H * d || s % vec)
+      return fail(RSWA_ERR_ARG, "%s: %s row stride %lld (at least H*d = %lld, a multiple of %lld)", who, name, s,
+                  (long long)H * d, vec);
+  if (x == y && sx != sy) return fail(RSWA_ERR_ARG, "%s: %s in place needs equal strides", who, name);
+  return RSWA_OK;
+}
+
+// Whether any row of [rows][H][d] tensor a (rows sa elements apart) meets any
+// row of b.  Rows interleaved in one buffer (equal strides) may alternate.
+static bool rows_overlap(const void* a, long long sa, long long na, const void* b, long long sb, long long nb, int rows,
+                         int elem) {
+  const long long d = ((long long)reinterpret_cast<uintptr_t>(b) - (long long)reinterpret_cast<uintptr_t>(a)) / elem;
+  if (d >= (rows - 1) * sa + na || -d >= (rows - 1) * sb + nb) return false;
+  if (sa != sb) return true;
+  const long long m = ((d % sa) + sa) % sa;  // b's row start within a's row
+  return m < na || m + nb > sa;
+}
+
+// A result is in place or meets no other tensor of the call.
+static rswa_status check_rotary_overlap(const char* who, const RotaryTensor* t, int rows, int d, int elem) {
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j) {
+      const RotaryTensor &a = t[i], &b = t[j];
+      if (!a.heads || !b.heads) continue;
+      const bool in_place = i == j && a.in == a.out;
+      if (!in_place && rows_overlap(a.out, a.out_stride, (long long)a.heads * d, b.in, b.in_stride,
+                                    (long long)b.heads * d, rows, elem))
+        return fail(RSWA_ERR_ARG, "%s: a result overlaps an input", who);
+      if (i < j && rows_overlap(a.out, a.out_stride, (long long)a.heads * d, b.out, b.out_stride,
+                                (long long)b.heads * d, rows, elem))
+        return fail(RSWA_ERR_ARG, "%s: the results overlap", who);
+    }
+  return RSWA_OK;
+}
+
+extern "C" rswa_status rswa_rotary_apply(const rswa_rotary* plan, const void* Q, long long q_stride, int H, void* Q_out,
+                                         long long q_out_stride, const void* K, long long k_stride, int H_k,
+                                         void* K_out, long long k_out_stride, const int32_t* positions, int first,
+                                         int rows, rswa_dtype dtype, int inverse, void* stream) {
+  static const char* who = "rswa_rotary_apply";
+  if (rswa_status st = check_rotary(who, plan)) return st;
+  if (!dtype_ok(dtype)) return fail(RSWA_ERR_UNSUPPORTED, "%s: unknown dtype", who);
+  if (rows < 1 || H < 1 || H_k < 0) return fail(RSWA_ERR_ARG, "%s: rows=%d H=%d H_k=%d", who, rows, H, H_k);
+  if (H > 32767 || H_k > 32767) return fail(RSWA_ERR_ARG, "%s: more than 32767 heads", who);
+  if (!positions && (first < 0 || (long long)first + rows > (1ll << 31)))
+    return fail(RSWA_ERR_ARG, "%s: positions %d .. outside [0, 2^31)", who, first);
+  if (reinterpret_cast<uintptr_t>(positions) & 3) return fail(RSWA_ERR_ARG, "%s: misaligned positions", who);
+  if (rswa_status st = check_rotary_tensor(who, "Q", Q, Q_out, q_stride, q_out_stride, H, plan->d, dtype)) return st;
+  if (H_k > 0)
+    if (rswa_status st = check_rotary_tensor(who, "K", K, K_out, k_stride, k_out_stride, H_k, plan->d, dtype)) return st;
+  const RotaryTensor t[2] = {{Q, Q_out, q_stride, q_out_stride, H}, {K, K_out, k_stride, k_out_stride, H_k}};
+  if (rswa_status st = check_rotary_overlap(who, t, rows, plan->d, elem_size(dtype))) return st;
+  RotaryParams p = {};
+  p.x[0] = t[0];
+  p.x[1] = t[1];
+  p.positions = positions;
+  p.first = first;
+  p.rows = rows;
+  p.sign = inverse ? -1.f : 1.f;
+  p.plan = *plan;
+  RSWA_CUDA(launch_rotary(p, dtype == RSWA_BF16 ? kBF16 : kF32, static_cast<cudaStream_t>(stream)), "rotary kernel");
+  return RSWA_OK;
+}
+
+extern "C" rswa_status rswa_rotary_step(rswa_handle h, const rswa_rotary* plan, const void* q, const void* k, void* q_out,
+                                        void* k_out) {
+  static const char* who = "rswa_rotary_step";
+  if (rswa_status st = check_handle(h)) return st;
+  if (rswa_status st = check_rotary(who, plan)) return st;
+  if (plan->d != h->d) return fail(RSWA_ERR_ARG, "%s: the plan's head dim %d, the handle's %d", who, plan->d, h->d);
+  const long long s = (long long)h->H * h->d;
+  if (rswa_status st = check_rotary_tensor(who, "q", q, q_out, s, s, h->H, h->d, h->dtype)) return st;
+  if (rswa_status st = check_rotary_tensor(who, "k", k, k_out, s, s, h->H, h->d, h->dtype)) return st;
+  if (!h->loaded) return fail(RSWA_ERR_STATE, "%s: no reference loaded", who);
+  if (rswa_status st = use_device(h)) return st;
+  const RotaryTensor t[2] = {{q, q_out, s, s, h->H}, {k, k_out, s, s, h->H}};
+  if (rswa_status st = check_rotary_overlap(who, t, h->B, h->d, elem_size(h->dtype))) return st;
+  RotaryParams p = {};
+  p.x[0] = t[0];
+  p.x[1] = t[1];
+  p.step_T = ws_i32(h, h->lay.T);
+  p.step_Lm = ws_i32(h, h->lay.Lm);
+  p.rows = h->B;
+  p.sign = 1.f;
+  p.plan = *plan;
+  RSWA_CUDA(launch_rotary(p, h->dtype == RSWA_BF16 ? kBF16 : kF32, h->stream), "rotary kernel");
   return RSWA_OK;
 }
 

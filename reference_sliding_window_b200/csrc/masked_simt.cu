@@ -85,6 +85,8 @@ masked_simt_kernel(const __grid_constant__ MaskedParams p) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   const float inv = 1.f / l;
+  // m and the scores are in log2 units
+  if (p.lse && lane == 0) p.lse[(size_t)h * p.lse_stride + row] = (m + log2f(l)) * 0.6931471805599453f;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) store_elem(O + row * hs + (size_t)h * D + lane + 32 * e, acc[e] * inv);
 }
