@@ -65,11 +65,7 @@ Plan make_plan(int size, const int32_t* cu, const int32_t* refs, int n_docs, int
   return plan;
 }
 
-int tile_size(int elem, int D) {
-  (void)elem;
-  (void)D;
-  return kBwdTileSimt;
-}
+int tile_size(int elem) { return elem == kBF16 ? kBwdTileTc : kBwdTileSimt; }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * (L + 128)); }
@@ -149,13 +145,13 @@ __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constan
 
 size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_docs, int n, int H, int D, int elem,
                                 bool bidir) {
-  const int size = tile_size(elem, D);
+  const int size = tile_size(elem);
   const Plan plan = make_plan(size, cu, refs, n_docs, n, H, bidir);
   return stats_bytes(cu[n_docs], H) + sizeof(float) * (size_t)plan.parts * H * 2 * size * D;
 }
 
 cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStream_t stream) {
-  const int size = tile_size(elem, p.D);
+  const int size = tile_size(elem);
   const Plan plan = make_plan(size, p.cu, p.refs, p.n_docs, p.n, p.H, p.bidir != 0);
   p.stats = static_cast<float2*>(workspace);
   p.stat_stride = p.L + 128;
@@ -164,7 +160,8 @@ cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStr
                   : p.D == 64  ? launch_stats<__nv_bfloat16, 64>(p, stream)
                                : launch_stats<__nv_bfloat16, 128>(p, stream);
   if (e != cudaSuccess) return e;
-  e = launch_backward_simt(p, elem, plan.work.data(), (int)plan.work.size(), stream);
+  e = elem == kBF16 ? launch_backward_tc(p, plan.work.data(), (int)plan.work.size(), stream)
+                    : launch_backward_simt(p, plan.work.data(), (int)plan.work.size(), stream);
   if (e != cudaSuccess) return e;
   JoinParams j;
   j.b = p;

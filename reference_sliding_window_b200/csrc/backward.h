@@ -98,7 +98,11 @@ size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_do
 // Fills the workspace fields of p from `workspace` (backward_workspace_bytes).
 cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStream_t stream);
 
-cudaError_t launch_backward_simt(const BackwardParams& p, int elem, const BwdWork* work, int n_work,
+// float32: the CUDA-core kernel.
+cudaError_t launch_backward_simt(const BackwardParams& p, const BwdWork* work, int n_work,
                                  cudaStream_t stream);
+
+// bf16, head dim 64 or 128: the tcgen05 kernel.
+cudaError_t launch_backward_tc(const BackwardParams& p, const BwdWork* work, int n_work, cudaStream_t stream);
 
 }  // namespace rswa

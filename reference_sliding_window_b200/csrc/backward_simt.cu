@@ -35,22 +35,14 @@ struct SimtParams {
 
 // Rows [row0, row0 + 64) of a packed [L][H][D] tensor's head h as float32;
 // rows at or past row_end are zero.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_tile(float* dst, const void* src, int row0, int row_end, int H, int h) {
-  constexpr int N = Vec16<T>::N;
-  for (int c = threadIdx.x; c < kT * (D / N); c += kThreads) {
-    const int r = c / (D / N), e = (c % (D / N)) * N;
-    float f[N];
-    if (row0 + r < row_end) {
-      const T* p = static_cast<const T*>(src) + ((size_t)(row0 + r) * H + h) * D + e;
-      Vec16<T>::unpack(*reinterpret_cast<const uint4*>(p), f);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      *reinterpret_cast<float4*>(dst + r * (D + 4) + e + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+  for (int c = threadIdx.x; c < kT * (D / 4); c += kThreads) {
+    const int r = c / (D / 4), e = (c % (D / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row0 + r < row_end)
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + ((size_t)(row0 + r) * H + h) * D + e);
+    *reinterpret_cast<float4*>(dst + r * (D + 4) + e) = v;
   }
 }
 
@@ -81,7 +73,7 @@ __device__ __forceinline__ void outer(float (*acc)[NC], float4 w, const float* r
 
 // A thread's 4 x NC block of a gradient tile (rows 4*ty .. +3, columns
 // tx*4 + 16*e .. +3), to the gradient or to a partial.
-template <typename T, int D, int NC>
+template <int D, int NC>
 __device__ __forceinline__ void write_tile(const float (*acc)[NC], void* grad, float* part, float mul, int row0,
                                            int row_end, int H, int h, int tx, int ty) {
 #pragma unroll
@@ -92,12 +84,12 @@ __device__ __forceinline__ void write_tile(const float (*acc)[NC], void* grad, f
     for (int e = 0; e < NC; ++e) {
       const int c = tx * 4 + 16 * (e & ~3) + (e & 3);
       if (part) part[r * D + c] = acc[a][e];
-      else store_elem(static_cast<T*>(grad) + ((size_t)(row0 + r) * H + h) * D + c, acc[a][e] * mul);
+      else static_cast<float*>(grad)[((size_t)(row0 + r) * H + h) * D + c] = acc[a][e] * mul;
     }
   }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const __grid_constant__ SimtParams p) {
   extern __shared__ __align__(16) float sm[];
   constexpr int S = D + 4, NC = D / 16;
@@ -116,8 +108,8 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const __grid_co
   const BwdTiles seq = dq ? bwd_key_tiles(kT, w.tile, w.len, w.ref, b.n, b.bidir != 0)
                           : bwd_query_tiles(kT, w.tile, w.len, w.ref, b.n, b.bidir != 0);
   const int end = w.start + w.len;
-  load_tile<T, D>(res0, dq ? b.Q : b.K, w.start + own0, end, b.H, h);
-  load_tile<T, D>(res1, dq ? b.dO : b.V, w.start + own0, end, b.H, h);
+  load_tile<D>(res0, dq ? b.Q : b.K, w.start + own0, end, b.H, h);
+  load_tile<D>(res1, dq ? b.dO : b.V, w.start + own0, end, b.H, h);
   const float* qs = dq ? res0 : str0;
   const float* gs = dq ? res1 : str1;
   const float* ks = dq ? str0 : res0;
@@ -131,8 +123,8 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const __grid_co
 
   for (int j = w.lo; j < w.hi; ++j) {
     const int other0 = seq.at(j) * kT;
-    load_tile<T, D>(str0, dq ? b.K : b.Q, w.start + other0, end, b.H, h);
-    load_tile<T, D>(str1, dq ? b.V : b.dO, w.start + other0, end, b.H, h);
+    load_tile<D>(str0, dq ? b.K : b.Q, w.start + other0, end, b.H, h);
+    load_tile<D>(str1, dq ? b.V : b.dO, w.start + other0, end, b.H, h);
     __syncthreads();
     const int q0 = dq ? own0 : other0, k0 = dq ? other0 : own0;
     float s[4][4], dp[4][4];
@@ -192,37 +184,34 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const __grid_co
   }
   float* part = w.part < 0 ? nullptr : b.partials + ((size_t)w.part * b.H + h) * 2 * kT * D;
   if (dq) {
-    write_tile<T, D, NC>(acc0, b.dQ, part, b.scale, w.start + own0, end, b.H, h, tx, ty);
+    write_tile<D, NC>(acc0, b.dQ, part, b.scale, w.start + own0, end, b.H, h, tx, ty);
   } else {
-    write_tile<T, D, NC>(acc0, b.dV, part, 1.f, w.start + own0, end, b.H, h, tx, ty);
-    write_tile<T, D, NC>(acc1, b.dK, part ? part + kT * D : nullptr, b.scale, w.start + own0, end, b.H, h, tx, ty);
+    write_tile<D, NC>(acc0, b.dV, part, 1.f, w.start + own0, end, b.H, h, tx, ty);
+    write_tile<D, NC>(acc1, b.dK, part ? part + kT * D : nullptr, b.scale, w.start + own0, end, b.H, h, tx, ty);
   }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t launch(const SimtParams& p, int n_work, cudaStream_t stream) {
   static PerContextOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(backward_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+    return cudaFuncSetAttribute(backward_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
   });
   if (e != cudaSuccess) return e;
-  backward_simt_kernel<T, D><<<n_work * p.b.H, kThreads, smem_bytes<D>(), stream>>>(p);
+  backward_simt_kernel<D><<<n_work * p.b.H, kThreads, smem_bytes<D>(), stream>>>(p);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_backward_simt(const BackwardParams& b, int elem, const BwdWork* work, int n_work,
-                                 cudaStream_t stream) {
+cudaError_t launch_backward_simt(const BackwardParams& b, const BwdWork* work, int n_work, cudaStream_t stream) {
   SimtParams p;
   p.b = b;
   p.scale_log2 = b.scale * 1.4426950408889634f;
   for (int w0 = 0; w0 < n_work; w0 += kBwdMaxWork) {
     const int m = n_work - w0 < kBwdMaxWork ? n_work - w0 : kBwdMaxWork;
     for (int i = 0; i < m; ++i) p.work[i] = work[w0 + i];
-    cudaError_t e = elem == kF32 ? (b.D == 64 ? launch<float, 64>(p, m, stream) : launch<float, 128>(p, m, stream))
-                    : b.D == 64  ? launch<__nv_bfloat16, 64>(p, m, stream)
-                                 : launch<__nv_bfloat16, 128>(p, m, stream);
+    const cudaError_t e = b.D == 64 ? launch<64>(p, m, stream) : launch<128>(p, m, stream);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

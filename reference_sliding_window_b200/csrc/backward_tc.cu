@@ -1,0 +1,494 @@
+// Gradient of the teacher-forced R-SWA attention on the 5th-generation tensor
+// cores (tcgen05 + TMEM): bf16 tensors, head dim 64 or 128, float32
+// accumulation.  The formulas, the mask and the work items are in backward.h.
+//
+// One CTA per work item and head, tiles of 128 queries x 128 keys.  Bound: the
+// tensor pipe (4 tile products per key tile and query tile in a dK, dV item, 3
+// in a dQ item), with the exponentials and the products' operand reads from
+// shared memory close behind.
+//
+// * A dK, dV item keeps its K and V tiles in shared memory and streams Q and
+//   dO tiles.  S and dP are formed transposed (keys on TMEM lanes), so that P
+//   and dS, bf16 pairs written over S's columns, are at once the A operands
+//   (read from TMEM) of dV += P^T dO and dK += dS^T Q, whose B operands are
+//   the streamed tiles themselves.
+// * A dQ item keeps Q and dO, streams K and V, and adds dQ += dS K with dS
+//   read from TMEM.
+// * Warp 0 streams tiles with TMA (128-byte swizzle) through two rings, warp
+//   1 issues the MMAs, warp 2 stages the row statistics (dK, dV items, where
+//   they vary along a thread's columns), warps 4-11 are the softmax: two
+//   groups of 128 threads, one thread per TMEM lane and half of its 128
+//   columns.
+// * Issue order of a dK, dV item, two score regions X, Y taking turns: S(i)
+//   in one, dP(i) in the other; while the softmax forms P(i) the tensor pipe
+//   runs dK(i-1) and dP(i), while it forms dS(i) it runs S(i+1), over the dP(i)
+//   just read, and dV(i).  A dQ item has two regions for S and one for dP, so
+//   S runs two tiles ahead.
+// * P and dS are rounded to bf16 for the products, as the tensor cores take
+//   them (relative error 2^-8 at most on each term of sums of independent
+//   terms); dS is formed from the float32 P.
+// * Rows of a streamed tile past the document's end belong to the next
+//   document.  Their weights are exactly 0, but 0 times an infinity is NaN, so
+//   the softmax clears them in shared memory before the products read them.
+// * Every wait is bounded; on a timeout the item's rows are written as NaN.
+
+#include <algorithm>
+
+#include "backward.h"
+#include "common.cuh"
+#include "tc.cuh"
+
+namespace rswa {
+namespace tc {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kSoftmaxWarp = 4;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kTmemCols = 512;
+
+struct BwdTcParams {
+  CUtensorMap tmQ, tmK, tmV, tmG;  // packed [L][H][D] maps; G is dO
+  BackwardParams b;
+  float scale_log2;
+  BwdWork work[kBwdMaxWork];  // heaviest first
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kBoxes = D / kBox;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  // ring A: K tiles (dQ items: read by S and, two tiles later, by dQ) or Q tiles; ring B: V or dO tiles
+  static constexpr int kAQ = D == 128 ? 3 : 4, kAKV = D == 128 ? 2 : 4, kB = D == 128 ? 2 : 4;
+  static constexpr int kSmRes = 0;
+  static constexpr int kSmA = kSmRes + 2 * kTileBytes;
+  static constexpr int kSmB = kSmA + kAQ * kTileBytes;
+  // statistics of the streamed query tiles (dK, dV items): where D = 128, in
+  // the third stage of ring A, which these items do not use
+  static constexpr int kSmStats = D == 128 ? kSmA + 2 * kTileBytes : kSmB + kB * kTileBytes;
+  static constexpr int kSmBar = kSmB + kB * kTileBytes + (D == 128 ? 0 : kAKV * 1024);
+  static constexpr int kSmBytes = kSmBar + 512 + 1024;  // + slack for 1024-byte alignment
+};
+
+enum : int {
+  kBarRes = 0,      // 2
+  kBarAFull = 2,    // 4
+  kBarAFree = 6,    // 4
+  kBarBFull = 10,   // 4
+  kBarBFree = 14,   // 4
+  kBarS = 18,       // 2
+  kBarDP = 20, kBarDPRead = 21, kBarP = 22, kBarDS = 23, kBarFinal = 24,
+  kBarStats = 25,   // 4
+  kSlotTmem = 30, kSlotAbort = 31
+};
+
+constexpr uint32_t idesc(int n, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24) |
+         (b_n_major ? 1u << 16 : 0u);
+}
+
+// D (TMEM) = A B^T over the head dim, both tiles K-major in shared memory.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t tmem_d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
+    mma_bf16(tmem_d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), idesc(kTile, false), kk > 0);
+  }
+}
+
+// D (TMEM, 128 x D) += A B: A 128 x 128 bf16 pairs in TMEM, its columns [0,
+// 64) at tmem_a and [64, 128) 64 TMEM columns on; B a tile's rows.
+template <int D>
+__device__ __forceinline__ void mma_grad(uint32_t tmem_d, uint32_t tmem_a, uint32_t b, bool acc) {
+#pragma unroll
+  for (int kk = 0; kk < kTile / 16; ++kk)
+    mma_bf16_ta(tmem_d, tmem_a + (kk >> 2) * 64 + (kk & 3) * 8, smem_desc(b + kk * 2048, kBoxBytes, 1024),
+                idesc(D, true), acc || kk > 0);
+}
+
+// 32 words of bf16 pairs into 32 TMEM columns of this thread's lane.
+__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t* w) {
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
+  tmem_st32(taddr, v);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_constant__ BwdTcParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kSmBar);
+  const uint32_t bar0 = smem_u32(bars);
+  auto B = [&](int slot) { return bar0 + 8u * slot; };
+  volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(&bars[kSlotTmem]);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(&bars[kSlotAbort]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  const int H = p.b.H, h = blockIdx.x % H;
+  const BwdWork w = p.work[blockIdx.x / H];
+  const bool dq = w.kind == kBwdDQ;
+  const bool bidir = p.b.bidir != 0;
+  const BwdTiles seq = dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir)
+                          : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir);
+  const int nt = w.hi - w.lo;
+  const int nA = dq ? C::kAQ : C::kAKV;
+  constexpr int nB = C::kB;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(B(kBarRes + s), 1);
+      mbar_init(B(kBarS + s), 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(B(kBarAFull + s), 1);
+      mbar_init(B(kBarAFree + s), 1);
+      mbar_init(B(kBarBFull + s), 1);
+      mbar_init(B(kBarBFree + s), 1);
+      mbar_init(B(kBarStats + s), 32);
+    }
+    mbar_init(B(kBarDP), 1);
+    mbar_init(B(kBarDPRead), kSoftmaxThreads);
+    mbar_init(B(kBarP), kSoftmaxThreads);
+    mbar_init(B(kBarDS), kSoftmaxThreads);
+    mbar_init(B(kBarFinal), 1);
+    *s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((const void*)s_tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      auto load = [&](uint32_t dst, const CUtensorMap* map, int tile, uint32_t bar) {
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+        for (int x = 0; x < C::kBoxes; ++x)
+          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, h, w.start + tile * kTile, bar);
+      };
+      const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
+      const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
+      load(smRes, dq ? &p.tmQ : &p.tmK, w.tile, B(kBarRes));
+      int a = 0, b = 0;  // tiles issued on each ring
+      bool ok = true;
+      for (int j = 0; j < nt && ok; ++j) {
+        const int tile = seq.at(w.lo + j);
+        ok = !*s_abort && mbar_wait_bounded(B(kBarAFree + j % nA), ((j / nA) & 1) ^ 1);
+        if (!ok) break;
+        load(smA + (j % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + j % nA));
+        ++a;
+        if (j == 0) load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, w.tile, B(kBarRes + 1));
+        ok = !*s_abort && mbar_wait_bounded(B(kBarBFree + j % nB), ((j / nB) & 1) ^ 1);
+        if (!ok) break;
+        load(smB + (j % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + j % nB));
+        ++b;
+      }
+      if (!ok) *s_abort = 1;
+      // drain: every issued copy has landed before the CTA may exit
+      mbar_wait_bounded(B(kBarRes), 0);
+      if (a > 0) mbar_wait_bounded(B(kBarRes + 1), 0);
+      for (int j = max(0, a - nA); j < a; ++j) mbar_wait_bounded(B(kBarAFull + j % nA), (j / nA) & 1);
+      for (int j = max(0, b - nB); j < b; ++j) mbar_wait_bounded(B(kBarBFull + j % nB), (j / nB) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      auto wait = [&](int slot, int phase) { return !*s_abort && mbar_wait_bounded(B(slot), phase & 1); };
+      auto tileA = [&](int j) { return smA + (j % nA) * C::kTileBytes; };
+      auto tileB = [&](int j) { return smB + (j % nB) * C::kTileBytes; };
+      bool ok;
+      if (dq) {
+        const uint32_t dP = tmem + 128, dQ = tmem + 384;
+        auto scores = [&](int j) -> bool {  // S(j) = Q K_j^T
+          if (!wait(kBarAFull + j % nA, j / nA)) return false;
+          tc_fence_after();
+          mma_scores<D>(tmem + (j & 1) * 256, smRes, tileA(j));
+          mma_commit(B(kBarS + (j & 1)));
+          return true;
+        };
+        auto dprob = [&](int j) -> bool {  // dP(j) = dO V_j^T
+          if (!wait(kBarBFull + j % nB, j / nB)) return false;
+          tc_fence_after();
+          mma_scores<D>(dP, smRes + C::kTileBytes, tileB(j));
+          mma_commit(B(kBarDP));
+          mma_commit(B(kBarBFree + j % nB));
+          return true;
+        };
+        ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0) && (nt < 2 || scores(1));
+        for (int j = 0; j < nt && ok; ++j) {
+          if (j + 1 < nt) ok = wait(kBarDPRead, j) && dprob(j + 1);
+          ok = ok && wait(kBarDS, j);
+          if (!ok) break;
+          tc_fence_after();
+          mma_grad<D>(dQ, tmem + (j & 1) * 256, tileA(j), j > 0);
+          mma_commit(B(kBarAFree + j % nA));
+          if (j + 2 < nt) ok = scores(j + 2);
+        }
+      } else {
+        const uint32_t dV = tmem + 256, dK = tmem + 384;
+        auto scores = [&](int j) -> bool {  // S(j)^T = K Q_j^T
+          if (!wait(kBarAFull + j % nA, j / nA)) return false;
+          tc_fence_after();
+          mma_scores<D>(tmem + (j & 1) * 128, smRes, tileA(j));
+          mma_commit(B(kBarS + (j & 1)));
+          return true;
+        };
+        auto dprob = [&](int j) -> bool {  // dP(j)^T = V dO_j^T
+          if (!wait(kBarBFull + j % nB, j / nB)) return false;
+          tc_fence_after();
+          mma_scores<D>(tmem + ((j & 1) ^ 1) * 128, smRes + C::kTileBytes, tileB(j));
+          mma_commit(B(kBarDP));
+          return true;
+        };
+        ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0);
+        for (int j = 0; j < nt && ok; ++j) {
+          if (j + 1 < nt) ok = wait(kBarDPRead, j) && scores(j + 1);
+          ok = ok && wait(kBarP, j);
+          if (!ok) break;
+          tc_fence_after();
+          mma_grad<D>(dV, tmem + (j & 1) * 128, tileB(j), j > 0);
+          mma_commit(B(kBarBFree + j % nB));
+          ok = wait(kBarDS, j);
+          if (!ok) break;
+          tc_fence_after();
+          mma_grad<D>(dK, tmem + (j & 1) * 128 + 32, tileA(j), j > 0);
+          mma_commit(B(kBarAFree + j % nA));
+          if (j + 1 < nt) ok = dprob(j + 1);
+        }
+      }
+      if (!ok) *s_abort = 1;
+      // every MMA issued by this thread has completed before TMEM is read or freed
+      mma_commit(B(kBarFinal));
+      mbar_wait_bounded(B(kBarFinal), 0);
+    }
+  } else if (warp == 2) {
+    // -------------------------------------------------- row statistics
+    if (!dq) {
+      for (int j = 0; j < nt; ++j) {
+        const int s = j % nA;
+        if (*s_abort || !mbar_wait_bounded(B(kBarAFree + s), ((j / nA) & 1) ^ 1)) break;
+        // rows past the document's end are another's, or padding of the array
+        const float2* src = p.b.stats + (size_t)h * p.b.stat_stride + w.start + seq.at(w.lo + j) * kTile;
+        float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = src[lane + 32 * i];
+          dst[lane + 32 * i] = v.x;
+          dst[kTile + lane + 32 * i] = v.y;
+        }
+        mbar_arrive(B(kBarStats + s));
+      }
+    }
+  } else if (warp >= kSoftmaxWarp) {
+    // ---------------------------------------------------------- softmax
+    const int g = (warp - kSoftmaxWarp) >> 2;  // column half
+    const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
+    const int r = quarter * 32 + lane;
+    const int c0 = 64 * g;
+    const int own = w.tile * kTile + r;        // local row: the thread's query (dQ) or key (dK, dV)
+    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+    const float sl2 = p.scale_log2;
+    float lse2 = 0.f, delta = 0.f;
+    if (dq && own < w.len) {
+      const float2 st = p.b.stats[(size_t)h * p.b.stat_stride + w.start + own];
+      lse2 = st.x;
+      delta = st.y;
+    }
+    bool ok = true;
+    // After a timed-out wait a thread stops waiting but keeps arriving, so
+    // the MMA thread is not left waiting on it; its rows are written as NaN.
+    auto wait = [&](int slot, int phase) {
+      if (ok && (*s_abort || !mbar_wait_bounded(B(slot), phase & 1))) ok = false;
+    };
+    for (int j = 0; j < nt; ++j) {
+      const int o0 = seq.at(w.lo + j) * kTile;  // first local row of the streamed tile
+      const uint32_t tS = base + (dq ? (j & 1) * 256 : (j & 1) * 128);
+      const uint32_t tP = base + (dq ? 128 : ((j & 1) ^ 1) * 128);
+      // The thread's visible columns: [lo, hi) and [lo2, hi2), tile columns.
+      int lo = 0, hi = kTile, lo2 = 0, hi2 = 0;
+      bool full;
+      if (dq) {
+        const int q0 = w.tile * kTile;
+        full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
+        if (!full) {
+          if (own < w.ref) {
+            hi = (bidir ? w.ref : own + 1) - o0;
+          } else {
+            hi = w.ref - o0;
+            lo2 = max(w.ref, own - p.b.n + 1) - o0;
+            hi2 = own + 1 - o0;
+          }
+        }
+      } else {
+        const int k0 = w.tile * kTile;
+        const int last = o0 + kTile - 1;
+        full = last < w.len && ((k0 + kTile <= w.ref && (bidir || k0 + kTile - 1 <= o0)) ||
+                                (k0 + kTile - 1 <= o0 && (long long)k0 + p.b.n > last));
+        if (!full) {
+          lo = (own < w.ref && bidir ? 0 : own) - o0;
+          hi = (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - o0;
+        }
+      }
+      const float* st = reinterpret_cast<const float*>(smem + C::kSmStats) + (j % nA) * 2 * kTile + c0;
+      if (!dq) wait(kBarStats + j % nA, j / nA);
+      wait(kBarS + (j & 1), j >> 1);
+      tc_fence_after();
+      float x[64];
+      tmem_ld32(tS, x);
+      tmem_ld32(tS + 32, x + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        float4 l4 = make_float4(lse2, lse2, lse2, lse2);
+        if (!dq) l4 = *reinterpret_cast<const float4*>(st + e);
+        x[e] = ex2(fmaf(x[e], sl2, -l4.x));
+        x[e + 1] = ex2(fmaf(x[e + 1], sl2, -l4.y));
+        x[e + 2] = ex2(fmaf(x[e + 2], sl2, -l4.z));
+        x[e + 3] = ex2(fmaf(x[e + 3], sl2, -l4.w));
+      }
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const int c = c0 + e;
+          x[e] = (c >= lo && c < hi) || (c >= lo2 && c < hi2) ? x[e] : 0.f;
+        }
+        // rows of the streamed tiles past the document's end
+        const int valid = w.len - o0;
+        if (valid < kTile) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
+            const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
+            const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
+            *reinterpret_cast<uint4*>(smem + C::kSmA + (j % nA) * C::kTileBytes + off) = zero;
+            if (!dq) *reinterpret_cast<uint4*>(smem + C::kSmB + (j % nB) * C::kTileBytes + off) = zero;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+      }
+      uint32_t pk[32];
+      if (!dq) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+        tmem_st_words(tS, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(B(kBarP));
+      }
+      wait(kBarDP, j);
+      tc_fence_after();
+      float dp[64];
+      tmem_ld32(tP, dp);
+      tmem_ld32(tP + 32, dp + 32);
+      tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(B(kBarDPRead));
+#pragma unroll
+      for (int e = 0; e < 64; e += 4) {
+        float4 d4 = make_float4(delta, delta, delta, delta);
+        if (!dq) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
+        x[e] *= dp[e] - d4.x;
+        x[e + 1] *= dp[e + 1] - d4.y;
+        x[e + 2] *= dp[e + 2] - d4.z;
+        x[e + 3] *= dp[e + 3] - d4.w;
+      }
+      if (!full) {  // a masked weight of 0 times a NaN of another document's row
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          const int c = c0 + e;
+          x[e] = (c >= lo && c < hi) || (c >= lo2 && c < hi2) ? x[e] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+      tmem_st_words(dq ? tS : tS + 32, pk);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(B(kBarDS));
+    }
+    // ------------------------------------------------ the tile's gradient
+    wait(kBarFinal, 0);
+    tc_fence_after();
+    if (!ok) *s_abort = 1;
+    const float nan = __int_as_float(0x7fc00000);
+    const bool good = ok && !*s_abort;
+    // dQ: each group half of the columns; dK, dV: group 0 dV, group 1 dK
+    constexpr int kHalfD = D / 2;
+    const int col0 = dq ? g * kHalfD : 0, cols = dq ? kHalfD : D;
+    const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (dq ? 384 + col0 : 256 + 128 * g);
+    float* part = w.part < 0 ? nullptr
+                             : p.b.partials + (((size_t)w.part * H + h) * 2 + (dq ? 0 : g)) * kTile * D + r * D + col0;
+    __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(dq ? p.b.dQ : g == 0 ? p.b.dV : p.b.dK) +
+                          ((size_t)(w.start + own) * H + h) * D + col0;
+    const float mul = !good ? nan : part || (!dq && g == 0) ? 1.f : p.b.scale;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+      float o[32];
+      tmem_ld32(src + c, o);
+      tmem_wait_ld();
+      if (own < w.len) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= mul;
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(grad + c + e) = pack16<__nv_bfloat16>(o + e);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                              : "memory");
+}
+
+template <int D>
+cudaError_t launch(const BwdTcParams& p, int n_work, cudaStream_t stream) {
+  static PerContextOnce once;
+  cudaError_t e = once.run([] {
+    return cudaFuncSetAttribute(backward_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmBytes);
+  });
+  if (e != cudaSuccess) return e;
+  backward_tc_kernel<D><<<n_work * p.b.H, kThreads, Cfg<D>::kSmBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace tc
+
+cudaError_t launch_backward_tc(const BackwardParams& b, const BwdWork* work, int n_work, cudaStream_t stream) {
+  using namespace tc;
+  BwdTcParams p;
+  if (!make_packed_map(&p.tmQ, b.Q, b.L, b.H, b.D) || !make_packed_map(&p.tmK, b.K, b.L, b.H, b.D) ||
+      !make_packed_map(&p.tmV, b.V, b.L, b.H, b.D) || !make_packed_map(&p.tmG, b.dO, b.L, b.H, b.D))
+    return cudaErrorInvalidValue;
+  p.b = b;
+  p.scale_log2 = b.scale * 1.4426950408889634f;
+  for (int w0 = 0; w0 < n_work; w0 += kBwdMaxWork) {
+    const int m = std::min(kBwdMaxWork, n_work - w0);
+    std::copy_n(work + w0, m, p.work);
+    const cudaError_t e = b.D == 64 ? launch<64>(p, m, stream) : launch<128>(p, m, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace rswa
