@@ -70,7 +70,7 @@ int tile_size(int elem) { return elem == kBF16 ? kBwdTileTc : kBwdTileSimt; }
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * (L + 128)); }
 
-// Row statistics (lse * log2 e, delta = O . dO), float32: D/N lanes per row
+// Row statistics, float32: D/N lanes per row
 // and head, 16 bytes of O and of dO each.  Bound by the reads of O and dO.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParams p) {
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParam
   for (int off = G / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (in && e == 0) {
     const int row = (int)(rh / p.H), h = (int)(rh % p.H);
-    p.stats[(size_t)h * p.stat_stride + row] = make_float2(p.lse[(size_t)h * p.L + row] * 1.4426950408889634f, sum);
+    p.stats[(size_t)h * p.stat_stride + row] = make_float2(p.lse[(size_t)h * p.L + row] * -1.4426950408889634f, -sum);
   }
 }
 

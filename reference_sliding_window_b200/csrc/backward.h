@@ -85,7 +85,7 @@ struct BackwardParams {
   const int32_t* refs;
   int n_docs;
   // workspace
-  float2* stats;    // [H][stat_stride]: (lse * log2 e, delta) of each row
+  float2* stats;    // [H][stat_stride]: (-lse log2 e, -delta) of each row
   int stat_stride;  // at least L + 128: a tile's rows may reach past the pack
   float* partials;  // [parts][H][2][tile][D]
 };

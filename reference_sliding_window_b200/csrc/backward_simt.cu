@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kThreads) backward_simt_kernel(const __grid_co
         const int kr = tx + 16 * c, key = k0 + kr;
         const bool vis = i < w.len && ((key <= i && (i < w.ref || key < w.ref || key > i - b.n)) ||
                                        (b.bidir && i < w.ref && key < w.ref));
-        const float pr = vis ? exp2f(fmaf(s[a][c], p.scale_log2, -st.x)) : 0.f;
-        const float ds = vis ? pr * (dp[a][c] - st.y) : 0.f;
+        const float pr = vis ? exp2f(fmaf(s[a][c], p.scale_log2, st.x)) : 0.f;
+        const float ds = vis ? pr * (dp[a][c] + st.y) : 0.f;
         if (dq) {
           t0[kr * kPS + r] = ds;
         } else {

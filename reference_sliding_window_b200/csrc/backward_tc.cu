@@ -70,6 +70,12 @@ struct Cfg {
   static constexpr int kSmBytes = kSmBar + 512 + 1024;  // + slack for 1024-byte alignment
 };
 
+// A wait names one of a barrier's two phases, so a barrier's next phase but one
+// must not complete while a waiter has still to see this one.  S, P and dS run
+// up to two tiles ahead of the MMA thread's or the softmax's waits (S(j+1) is
+// issued before P(j) is awaited; a dQ item's dS(j+1) needs nothing that follows
+// the wait for dS(j)) and take two barriers in turn; everything else is
+// ordered by the ring's or the region's next use.
 enum : int {
   kBarRes = 0,      // 2
   kBarAFull = 2,    // 4
@@ -77,9 +83,11 @@ enum : int {
   kBarBFull = 10,   // 4
   kBarBFree = 14,   // 4
   kBarS = 18,       // 2
-  kBarDP = 20, kBarDPRead = 21, kBarP = 22, kBarDS = 23, kBarFinal = 24,
-  kBarStats = 25,   // 4
-  kSlotTmem = 30, kSlotAbort = 31
+  kBarP = 20,       // 2
+  kBarDS = 22,      // 2
+  kBarDP = 24, kBarDPRead = 25, kBarFinal = 26,
+  kBarStats = 27,   // 4
+  kSlotTmem = 31, kSlotAbort = 32
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -107,12 +115,229 @@ __device__ __forceinline__ void mma_grad(uint32_t tmem_d, uint32_t tmem_a, uint3
                 idesc(D, true), acc || kk > 0);
 }
 
-// 32 words of bf16 pairs into 32 TMEM columns of this thread's lane.
+// 16 words of bf16 pairs into 16 TMEM columns of this thread's lane.
 __device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t* w) {
-  float v[32];
+  float v[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(w[i]);
-  tmem_st32(taddr, v);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
+  tmem_st16(taddr, v);
+}
+
+// Two floats at a time (the same roundings per element).
+__device__ __forceinline__ void fma2(float& x0, float& x1, float m, float a0, float a1) {
+  unsigned long long x, mm, a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(mm) : "f"(m));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(mm), "l"(a));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(x));
+}
+// p *= x + a
+__device__ __forceinline__ void addmul2(float& p0, float& p1, float x0, float x1, float a0, float a1) {
+  unsigned long long p, x, a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(p0), "f"(p1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(a));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(p) : "l"(x));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(p0), "=f"(p1) : "l"(p));
+}
+
+// Bits [lo, hi) of 64.
+__device__ __forceinline__ unsigned long long bit_range(int lo, int hi) {
+  const unsigned long long below_hi = hi <= 0 ? 0ull : hi >= 64 ? ~0ull : (1ull << hi) - 1;
+  const unsigned long long below_lo = lo <= 0 ? 0ull : lo >= 64 ? ~0ull : (1ull << lo) - 1;
+  return below_hi & ~below_lo;
+}
+// N elements zeroed (whatever they hold, NaN included) where their bit is clear.
+template <int N>
+__device__ __forceinline__ void keep(float* x, uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    x[e] = __uint_as_float(__float_as_uint(x[e]) & (uint32_t)((int)(bits << (31 - e)) >> 31));
+}
+
+struct Ctx {
+  const BwdTcParams& p;
+  const BwdWork& w;
+  const BwdTiles& seq;
+  uint8_t* smem;
+  uint32_t bar0, tmem;
+  volatile int* abort;
+  int h;
+};
+
+// The softmax warps of an item: P and dS of every tile of its sequence, then
+// the finished gradient tile from TMEM to memory.
+template <int D, bool DQ>
+__device__ __forceinline__ void softmax_warps(const Ctx& c) {
+  using C = Cfg<D>;
+  constexpr int nA = DQ ? C::kAQ : C::kAKV, nB = C::kB;
+  const BwdTcParams& p = c.p;
+  const BwdWork& w = c.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = (warp - kSoftmaxWarp) >> 2;  // column half
+  const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
+  const int r = quarter * 32 + lane;
+  const int c0 = 64 * g;
+  const int own = w.tile * kTile + r;        // local row: the thread's query (DQ) or key
+  const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+  const float sl2 = p.scale_log2;
+  const bool bidir = p.b.bidir != 0;
+  float nlse = 0.f, ndelta = 0.f;
+  if (DQ && own < w.len) {
+    const float2 st = p.b.stats[(size_t)c.h * p.b.stat_stride + w.start + own];
+    nlse = st.x;
+    ndelta = st.y;
+  }
+  bool ok = true;
+  // After a timed-out wait a thread stops waiting but keeps arriving, so
+  // the MMA thread is not left waiting on it; its rows are written as NaN.
+  auto wait = [&](int slot, int phase) {
+    if (ok && (*c.abort || !mbar_wait_bounded(c.bar0 + 8u * slot, phase & 1))) ok = false;
+  };
+  // A warp's arrival, once all of its lanes are there: an arrival per lane
+  // costs an operation on the barrier's word each.
+  auto arrive = [&](int slot) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar0 + 8u * slot);
+  };
+  for (int j = w.lo; j < w.hi; ++j) {
+    const int it = j - w.lo;
+    const int o0 = c.seq.at(j) * kTile;  // first local row of the streamed tile
+    const uint32_t tS = base + (DQ ? (it & 1) * 256 : (it & 1) * 128);
+    const uint32_t tP = base + (DQ ? 128 : ((it & 1) ^ 1) * 128);
+    // whether every pair of the tiles is visible; otherwise the thread's
+    // visible columns
+    bool full;
+    unsigned long long vis = ~0ull;
+    if (DQ) {
+      const int q0 = w.tile * kTile;
+      full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
+      if (!full) {
+        if (own < w.ref) {
+          vis = bit_range(0, (bidir ? w.ref : own + 1) - o0 - c0);
+        } else {
+          vis = bit_range(0, w.ref - o0 - c0) |
+                bit_range(max(w.ref, own - p.b.n + 1) - o0 - c0, own + 1 - o0 - c0);
+        }
+      }
+    } else {
+      const int k0 = w.tile * kTile, last = o0 + kTile - 1;
+      full = last < w.len && ((k0 + kTile <= w.ref && (bidir || k0 + kTile - 1 <= o0)) ||
+                              (k0 + kTile - 1 <= o0 && (long long)k0 + p.b.n > last));
+      if (!full)
+        vis = bit_range((own < w.ref && bidir ? 0 : own) - o0 - c0,
+                        (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - o0 - c0);
+    }
+    const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it % nA) * 2 * kTile + c0;
+    if (!DQ) wait(kBarStats + it % nA, it / nA);
+    wait(kBarS + (it & 1), it >> 1);
+    tc_fence_after();
+    float x[64];
+    tmem_ld32(tS, x);
+    tmem_ld32(tS + 32, x + 32);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 64; e += 4) {
+      float4 l4 = make_float4(nlse, nlse, nlse, nlse);
+      if (!DQ) l4 = *reinterpret_cast<const float4*>(st + e);
+      fma2(x[e], x[e + 1], sl2, l4.x, l4.y);
+      fma2(x[e + 2], x[e + 3], sl2, l4.z, l4.w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[e + i] = ex2(x[e + i]);
+    }
+    if (!full) {
+      keep<32>(x, (uint32_t)vis);
+      keep<32>(x + 32, (uint32_t)(vis >> 32));
+      // rows of the streamed tiles past the document's end
+      const int valid = w.len - o0;
+      if (valid < kTile) {
+        for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
+          const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
+          const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(c.smem + C::kSmA + (it % nA) * C::kTileBytes + off) = zero;
+          if (!DQ) *reinterpret_cast<uint4*>(c.smem + C::kSmB + (it % nB) * C::kTileBytes + off) = zero;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+    }
+    if (!DQ) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]);
+        tmem_st_words(tS + 16 * q, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      arrive(kBarP + (it & 1));
+    }
+    wait(kBarDP, it);
+    tc_fence_after();
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float dp[32];
+      tmem_ld32(tP + 32 * q, dp);
+      tmem_wait_ld();
+      if (q == 1) {
+        tc_fence_before();
+        arrive(kBarDPRead);
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+        if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + 32 * q + e);
+        float* y = x + 32 * q + e;
+        addmul2(y[0], y[1], dp[e], dp[e + 1], d4.x, d4.y);
+        addmul2(y[2], y[3], dp[e + 2], dp[e + 3], d4.z, d4.w);
+      }
+      // a masked weight of 0 times a NaN of another document's row
+      if (!full) keep<32>(x + 32 * q, (uint32_t)(vis >> (32 * q)));
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]);
+      tmem_st_words((DQ ? tS : tS + 32) + 16 * q, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    arrive(kBarDS + (it & 1));
+  }
+  // -------------------------------------------------- the tile's gradient
+  wait(kBarFinal, 0);
+  tc_fence_after();
+  if (!ok) *c.abort = 1;
+  const bool good = ok && !*c.abort;
+  // dQ: each group half of the columns; dK, dV: group 0 dV, group 1 dK
+  constexpr int kCols = DQ ? D / 2 : D;
+  const int col0 = DQ ? g * kCols : 0;
+  const uint32_t src = c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 + col0 : 256 + 128 * g);
+  const int H = p.b.H;
+  float* part = w.part < 0 ? nullptr
+                           : p.b.partials + (((size_t)w.part * H + c.h) * 2 + (DQ ? 0 : g)) * kTile * D + r * D + col0;
+  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : g == 0 ? p.b.dV : p.b.dK) +
+                        ((size_t)(w.start + own) * H + c.h) * D + col0;
+  const float mul = !good ? __int_as_float(0x7fc00000) : part || (!DQ && g == 0) ? 1.f : p.b.scale;
+#pragma unroll 1
+  for (int k = 0; k < kCols; k += 32) {
+    float o[32];
+    tmem_ld32(src + k, o);
+    tmem_wait_ld();
+    if (own < w.len) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] *= mul;
+      if (part) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(part + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(grad + k + e) = pack16<__nv_bfloat16>(o + e);
+      }
+    }
+  }
 }
 
 template <int D>
@@ -142,18 +367,18 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     for (int s = 0; s < 2; ++s) {
       mbar_init(B(kBarRes + s), 1);
       mbar_init(B(kBarS + s), 1);
+      mbar_init(B(kBarP + s), kSoftmaxThreads / 32);
+      mbar_init(B(kBarDS + s), kSoftmaxThreads / 32);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(B(kBarAFull + s), 1);
       mbar_init(B(kBarAFree + s), 1);
       mbar_init(B(kBarBFull + s), 1);
       mbar_init(B(kBarBFree + s), 1);
-      mbar_init(B(kBarStats + s), 32);
+      mbar_init(B(kBarStats + s), 1);
     }
     mbar_init(B(kBarDP), 1);
-    mbar_init(B(kBarDPRead), kSoftmaxThreads);
-    mbar_init(B(kBarP), kSoftmaxThreads);
-    mbar_init(B(kBarDS), kSoftmaxThreads);
+    mbar_init(B(kBarDPRead), kSoftmaxThreads / 32);
     mbar_init(B(kBarFinal), 1);
     *s_abort = 0;
     fence_barrier_init();
@@ -230,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0) && (nt < 2 || scores(1));
         for (int j = 0; j < nt && ok; ++j) {
           if (j + 1 < nt) ok = wait(kBarDPRead, j) && dprob(j + 1);
-          ok = ok && wait(kBarDS, j);
+          ok = ok && wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           mma_grad<D>(dQ, tmem + (j & 1) * 256, tileA(j), j > 0);
@@ -256,12 +481,12 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0);
         for (int j = 0; j < nt && ok; ++j) {
           if (j + 1 < nt) ok = wait(kBarDPRead, j) && scores(j + 1);
-          ok = ok && wait(kBarP, j);
+          ok = ok && wait(kBarP + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           mma_grad<D>(dV, tmem + (j & 1) * 128, tileB(j), j > 0);
           mma_commit(B(kBarBFree + j % nB));
-          ok = wait(kBarDS, j);
+          ok = wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           mma_grad<D>(dK, tmem + (j & 1) * 128 + 32, tileA(j), j > 0);
@@ -279,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     if (!dq) {
       for (int j = 0; j < nt; ++j) {
         const int s = j % nA;
-        if (*s_abort || !mbar_wait_bounded(B(kBarAFree + s), ((j / nA) & 1) ^ 1)) break;
+        if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait_bounded(B(kBarAFree + s), ((j / nA) & 1) ^ 1))) break;
         // rows past the document's end are another's, or padding of the array
         const float2* src = p.b.stats + (size_t)h * p.b.stat_stride + w.start + seq.at(w.lo + j) * kTile;
         float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
@@ -289,169 +514,14 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
           dst[lane + 32 * i] = v.x;
           dst[kTile + lane + 32 * i] = v.y;
         }
-        mbar_arrive(B(kBarStats + s));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B(kBarStats + s));
       }
     }
   } else if (warp >= kSoftmaxWarp) {
-    // ---------------------------------------------------------- softmax
-    const int g = (warp - kSoftmaxWarp) >> 2;  // column half
-    const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
-    const int r = quarter * 32 + lane;
-    const int c0 = 64 * g;
-    const int own = w.tile * kTile + r;        // local row: the thread's query (dQ) or key (dK, dV)
-    const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-    const float sl2 = p.scale_log2;
-    float lse2 = 0.f, delta = 0.f;
-    if (dq && own < w.len) {
-      const float2 st = p.b.stats[(size_t)h * p.b.stat_stride + w.start + own];
-      lse2 = st.x;
-      delta = st.y;
-    }
-    bool ok = true;
-    // After a timed-out wait a thread stops waiting but keeps arriving, so
-    // the MMA thread is not left waiting on it; its rows are written as NaN.
-    auto wait = [&](int slot, int phase) {
-      if (ok && (*s_abort || !mbar_wait_bounded(B(slot), phase & 1))) ok = false;
-    };
-    for (int j = 0; j < nt; ++j) {
-      const int o0 = seq.at(w.lo + j) * kTile;  // first local row of the streamed tile
-      const uint32_t tS = base + (dq ? (j & 1) * 256 : (j & 1) * 128);
-      const uint32_t tP = base + (dq ? 128 : ((j & 1) ^ 1) * 128);
-      // The thread's visible columns: [lo, hi) and [lo2, hi2), tile columns.
-      int lo = 0, hi = kTile, lo2 = 0, hi2 = 0;
-      bool full;
-      if (dq) {
-        const int q0 = w.tile * kTile;
-        full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
-        if (!full) {
-          if (own < w.ref) {
-            hi = (bidir ? w.ref : own + 1) - o0;
-          } else {
-            hi = w.ref - o0;
-            lo2 = max(w.ref, own - p.b.n + 1) - o0;
-            hi2 = own + 1 - o0;
-          }
-        }
-      } else {
-        const int k0 = w.tile * kTile;
-        const int last = o0 + kTile - 1;
-        full = last < w.len && ((k0 + kTile <= w.ref && (bidir || k0 + kTile - 1 <= o0)) ||
-                                (k0 + kTile - 1 <= o0 && (long long)k0 + p.b.n > last));
-        if (!full) {
-          lo = (own < w.ref && bidir ? 0 : own) - o0;
-          hi = (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - o0;
-        }
-      }
-      const float* st = reinterpret_cast<const float*>(smem + C::kSmStats) + (j % nA) * 2 * kTile + c0;
-      if (!dq) wait(kBarStats + j % nA, j / nA);
-      wait(kBarS + (j & 1), j >> 1);
-      tc_fence_after();
-      float x[64];
-      tmem_ld32(tS, x);
-      tmem_ld32(tS + 32, x + 32);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-        float4 l4 = make_float4(lse2, lse2, lse2, lse2);
-        if (!dq) l4 = *reinterpret_cast<const float4*>(st + e);
-        x[e] = ex2(fmaf(x[e], sl2, -l4.x));
-        x[e + 1] = ex2(fmaf(x[e + 1], sl2, -l4.y));
-        x[e + 2] = ex2(fmaf(x[e + 2], sl2, -l4.z));
-        x[e + 3] = ex2(fmaf(x[e + 3], sl2, -l4.w));
-      }
-      if (!full) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const int c = c0 + e;
-          x[e] = (c >= lo && c < hi) || (c >= lo2 && c < hi2) ? x[e] : 0.f;
-        }
-        // rows of the streamed tiles past the document's end
-        const int valid = w.len - o0;
-        if (valid < kTile) {
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
-            const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
-            const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
-            *reinterpret_cast<uint4*>(smem + C::kSmA + (j % nA) * C::kTileBytes + off) = zero;
-            if (!dq) *reinterpret_cast<uint4*>(smem + C::kSmB + (j % nB) * C::kTileBytes + off) = zero;
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-      }
-      uint32_t pk[32];
-      if (!dq) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-        tmem_st_words(tS, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(B(kBarP));
-      }
-      wait(kBarDP, j);
-      tc_fence_after();
-      float dp[64];
-      tmem_ld32(tP, dp);
-      tmem_ld32(tP + 32, dp + 32);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(B(kBarDPRead));
-#pragma unroll
-      for (int e = 0; e < 64; e += 4) {
-        float4 d4 = make_float4(delta, delta, delta, delta);
-        if (!dq) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
-        x[e] *= dp[e] - d4.x;
-        x[e + 1] *= dp[e + 1] - d4.y;
-        x[e + 2] *= dp[e + 2] - d4.z;
-        x[e + 3] *= dp[e + 3] - d4.w;
-      }
-      if (!full) {  // a masked weight of 0 times a NaN of another document's row
-#pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const int c = c0 + e;
-          x[e] = (c >= lo && c < hi) || (c >= lo2 && c < hi2) ? x[e] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-      tmem_st_words(dq ? tS : tS + 32, pk);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(B(kBarDS));
-    }
-    // ------------------------------------------------ the tile's gradient
-    wait(kBarFinal, 0);
-    tc_fence_after();
-    if (!ok) *s_abort = 1;
-    const float nan = __int_as_float(0x7fc00000);
-    const bool good = ok && !*s_abort;
-    // dQ: each group half of the columns; dK, dV: group 0 dV, group 1 dK
-    constexpr int kHalfD = D / 2;
-    const int col0 = dq ? g * kHalfD : 0, cols = dq ? kHalfD : D;
-    const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (dq ? 384 + col0 : 256 + 128 * g);
-    float* part = w.part < 0 ? nullptr
-                             : p.b.partials + (((size_t)w.part * H + h) * 2 + (dq ? 0 : g)) * kTile * D + r * D + col0;
-    __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(dq ? p.b.dQ : g == 0 ? p.b.dV : p.b.dK) +
-                          ((size_t)(w.start + own) * H + h) * D + col0;
-    const float mul = !good ? nan : part || (!dq && g == 0) ? 1.f : p.b.scale;
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-      float o[32];
-      tmem_ld32(src + c, o);
-      tmem_wait_ld();
-      if (own < w.len) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= mul;
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(grad + c + e) = pack16<__nv_bfloat16>(o + e);
-        }
-      }
-    }
+    const Ctx c{p, w, seq, smem, bar0, tmem, s_abort, h};
+    if (dq) softmax_warps<D, true>(c);
+    else softmax_warps<D, false>(c);
   }
   tc_fence_before();
   __syncthreads();
