@@ -95,24 +95,55 @@ constexpr uint32_t idesc(int n, bool b_n_major) {
          (b_n_major ? 1u << 16 : 0u);
 }
 
+// The MMA warp runs these with all lanes, so that descriptors and addresses
+// stay in uniform registers; the instruction itself issues on the one lane
+// with lead != 0 (always the same: a commit covers its own thread's MMAs).
+__device__ __forceinline__ void mma_ss(int lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(int lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(int lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
+      : "memory");
+}
+
 // D (TMEM) = A B^T over the head dim, both tiles K-major in shared memory.
 template <int D>
-__device__ __forceinline__ void mma_scores(uint32_t tmem_d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void mma_scores(int lead, uint32_t tmem_d, uint32_t a, uint32_t b) {
+  const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(b, 16, 1024);
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * kBoxBytes + (kk & 3) * 32;
-    mma_bf16(tmem_d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), idesc(kTile, false), kk > 0);
+    const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
+    mma_ss(lead, tmem_d, da + off, db + off, idesc(kTile, false), kk > 0);
   }
 }
 
 // D (TMEM, 128 x D) += A B: A 128 x 128 bf16 pairs in TMEM, its columns [0,
 // 64) at tmem_a and [64, 128) 64 TMEM columns on; B a tile's rows.
 template <int D>
-__device__ __forceinline__ void mma_grad(uint32_t tmem_d, uint32_t tmem_a, uint32_t b, bool acc) {
+__device__ __forceinline__ void mma_grad(int lead, uint32_t tmem_d, uint32_t tmem_a, uint32_t b, bool acc) {
+  const uint64_t db = smem_desc(b, kBoxBytes, 1024);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_bf16_ta(tmem_d, tmem_a + (kk >> 2) * 64 + (kk & 3) * 8, smem_desc(b + kk * 2048, kBoxBytes, 1024),
-                idesc(D, true), acc || kk > 0);
+    mma_ts(lead, tmem_d, tmem_a + (kk >> 2) * 64 + (kk & 3) * 8, db + ((kk * 2048) >> 4), idesc(D, true),
+           kk > 0 ? 1u : acc);
 }
 
 // 16 words of bf16 pairs into 16 TMEM columns of this thread's lane.
@@ -277,22 +308,20 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     }
     wait(kBarDP, it);
     tc_fence_after();
+    float dp[64];
+    tmem_ld32(tP, dp);
+    tmem_ld32(tP + 32, dp + 32);
+    tmem_wait_ld();
+    tc_fence_before();
+    arrive(kBarDPRead);
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      float dp[32];
-      tmem_ld32(tP + 32 * q, dp);
-      tmem_wait_ld();
-      if (q == 1) {
-        tc_fence_before();
-        arrive(kBarDPRead);
-      }
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
+      for (int e = 32 * q; e < 32 * q + 32; e += 4) {
         float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-        if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + 32 * q + e);
-        float* y = x + 32 * q + e;
-        addmul2(y[0], y[1], dp[e], dp[e + 1], d4.x, d4.y);
-        addmul2(y[2], y[3], dp[e + 2], dp[e + 3], d4.z, d4.w);
+        if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
+        addmul2(x[e], x[e + 1], dp[e], dp[e + 1], d4.x, d4.y);
+        addmul2(x[e + 2], x[e + 3], dp[e + 2], dp[e + 3], d4.z, d4.w);
       }
       // a masked weight of 0 times a NaN of another document's row
       if (!full) keep<32>(x + 32 * q, (uint32_t)(vis >> (32 * q)));
@@ -430,8 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      auto wait = [&](int slot, int phase) { return !*s_abort && mbar_wait_bounded(B(slot), phase & 1); };
+    {
+      const int lead = lane == 0;
+      // (every lane of the warp answers the same)
+      auto wait = [&](int slot, int phase) {
+        return __all_sync(0xffffffffu, !*s_abort && mbar_wait_bounded(B(slot), phase & 1)) != 0;
+      };
       auto tileA = [&](int j) { return smA + (j % nA) * C::kTileBytes; };
       auto tileB = [&](int j) { return smB + (j % nB) * C::kTileBytes; };
       bool ok;
@@ -440,16 +473,16 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         auto scores = [&](int j) -> bool {  // S(j) = Q K_j^T
           if (!wait(kBarAFull + j % nA, j / nA)) return false;
           tc_fence_after();
-          mma_scores<D>(tmem + (j & 1) * 256, smRes, tileA(j));
-          mma_commit(B(kBarS + (j & 1)));
+          mma_scores<D>(lead, tmem + (j & 1) * 256, smRes, tileA(j));
+          commit(lead, B(kBarS + (j & 1)));
           return true;
         };
         auto dprob = [&](int j) -> bool {  // dP(j) = dO V_j^T
           if (!wait(kBarBFull + j % nB, j / nB)) return false;
           tc_fence_after();
-          mma_scores<D>(dP, smRes + C::kTileBytes, tileB(j));
-          mma_commit(B(kBarDP));
-          mma_commit(B(kBarBFree + j % nB));
+          mma_scores<D>(lead, dP, smRes + C::kTileBytes, tileB(j));
+          commit(lead, B(kBarDP));
+          commit(lead, B(kBarBFree + j % nB));
           return true;
         };
         ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0) && (nt < 2 || scores(1));
@@ -458,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
           ok = ok && wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(dQ, tmem + (j & 1) * 256, tileA(j), j > 0);
-          mma_commit(B(kBarAFree + j % nA));
+          mma_grad<D>(lead, dQ, tmem + (j & 1) * 256, tileA(j), j > 0);
+          commit(lead, B(kBarAFree + j % nA));
           if (j + 2 < nt) ok = scores(j + 2);
         }
       } else {
@@ -467,15 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
         auto scores = [&](int j) -> bool {  // S(j)^T = K Q_j^T
           if (!wait(kBarAFull + j % nA, j / nA)) return false;
           tc_fence_after();
-          mma_scores<D>(tmem + (j & 1) * 128, smRes, tileA(j));
-          mma_commit(B(kBarS + (j & 1)));
+          mma_scores<D>(lead, tmem + (j & 1) * 128, smRes, tileA(j));
+          commit(lead, B(kBarS + (j & 1)));
           return true;
         };
         auto dprob = [&](int j) -> bool {  // dP(j)^T = V dO_j^T
           if (!wait(kBarBFull + j % nB, j / nB)) return false;
           tc_fence_after();
-          mma_scores<D>(tmem + ((j & 1) ^ 1) * 128, smRes + C::kTileBytes, tileB(j));
-          mma_commit(B(kBarDP));
+          mma_scores<D>(lead, tmem + ((j & 1) ^ 1) * 128, smRes + C::kTileBytes, tileB(j));
+          commit(lead, B(kBarDP));
           return true;
         };
         ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0);
@@ -484,19 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
           ok = ok && wait(kBarP + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(dV, tmem + (j & 1) * 128, tileB(j), j > 0);
-          mma_commit(B(kBarBFree + j % nB));
+          mma_grad<D>(lead, dV, tmem + (j & 1) * 128, tileB(j), j > 0);
+          commit(lead, B(kBarBFree + j % nB));
           ok = wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(dK, tmem + (j & 1) * 128 + 32, tileA(j), j > 0);
-          mma_commit(B(kBarAFree + j % nA));
+          mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + 32, tileA(j), j > 0);
+          commit(lead, B(kBarAFree + j % nA));
           if (j + 1 < nt) ok = dprob(j + 1);
         }
       }
       if (!ok) *s_abort = 1;
       // every MMA issued by this thread has completed before TMEM is read or freed
-      mma_commit(B(kBarFinal));
+      commit(lead, B(kBarFinal));
       mbar_wait_bounded(B(kBarFinal), 0);
     }
   } else if (warp == 2) {
