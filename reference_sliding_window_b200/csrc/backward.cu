@@ -65,7 +65,7 @@ Plan make_plan(int size, const int32_t* cu, const int32_t* refs, int n_docs, int
   return plan;
 }
 
-int tile_size(int elem) { return elem == kBF16 ? kBwdTileTc : kBwdTileSimt; }
+int tile_size(int elem) { return elem == kBF16 ? kBwdTileTc : kBwdTileF32; }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
 size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * (L + 128)); }
@@ -161,7 +161,7 @@ cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStr
                                : launch_stats<__nv_bfloat16, 128>(p, stream);
   if (e != cudaSuccess) return e;
   e = elem == kBF16 ? launch_backward_tc(p, plan.work.data(), (int)plan.work.size(), stream)
-                    : launch_backward_simt(p, plan.work.data(), (int)plan.work.size(), stream);
+                    : launch_backward_f32(p, plan.work.data(), (int)plan.work.size(), stream);
   if (e != cudaSuccess) return e;
   JoinParams j;
   j.b = p;

@@ -90,7 +90,7 @@ struct BackwardParams {
   float* partials;  // [parts][H][2][tile][D]
 };
 
-constexpr int kBwdTileTc = 128, kBwdTileSimt = 64;
+constexpr int kBwdTileTc = 128, kBwdTileF32 = 64;
 constexpr int kBwdMaxWork = 960;  // work entries per launch (30 KB of kernel parameters)
 
 size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_docs, int n, int H, int D, int elem,
@@ -98,8 +98,8 @@ size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_do
 // Fills the workspace fields of p from `workspace` (backward_workspace_bytes).
 cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStream_t stream);
 
-// float32: the CUDA-core kernel.
-cudaError_t launch_backward_simt(const BackwardParams& p, const BwdWork* work, int n_work,
+// float32: three tf32 MMAs per product.
+cudaError_t launch_backward_f32(const BackwardParams& p, const BwdWork* work, int n_work,
                                  cudaStream_t stream);
 
 // bf16, head dim 64 or 128: the tcgen05 kernel.
