@@ -63,6 +63,28 @@ def _check_tensor(name: str, t: torch.Tensor, shape, dtype, device) -> None:
         raise ValueError(f"{name} must be contiguous")
 
 
+_device_now = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(index: int, fn, *args) -> None:
+    """fn(*args) with CUDA device `index` current; raises on its status."""
+    if _device_now() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status:
+        check(status)
+
+
+def _check_like(name: str, t: torch.Tensor, like: torch.Tensor, shape, index: int) -> None:
+    """t has like's dtype, this shape, device `index` and is contiguous: in one
+    pass over cached values, or by the check that names the problem."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
+        _check_tensor(name, t, shape, like.dtype, like.device)
+
+
 class RSWA:
     """Decode-side R-SWA state over caller-owned device memory.
 
@@ -227,7 +249,7 @@ class RSWA:
         self._vec("out[0]", qo)
         self._vec("out[1]", ko)
         self._sync_stream()
-        check(self._lib.rswa_rotary_step(self._h, rotary._plan, q.data_ptr(), k.data_ptr(), qo.data_ptr(),
+        check(self._lib.rswa_rotary_step(self._h, rotary._ref, q.data_ptr(), k.data_ptr(), qo.data_ptr(),
                                          ko.data_ptr()))
         return qo, ko
 
@@ -361,6 +383,8 @@ class LayerStep:
 
 def _pack_args(Q: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[int]):
     """Checks Q and the documents; -> (L, H, d, cu, refs) with the host arrays as ctypes."""
+    if not Q.is_cuda:
+        raise ValueError(f"Q is on {Q.device}, expected a CUDA device")
     if Q.dim() != 3:
         raise ValueError("Q must be [L, H, d]")
     L, H, d = Q.shape
@@ -374,16 +398,14 @@ def _pack_args(Q: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[in
 
 def _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, out, bidir_prefix):
     L, H, d, cu, refs = _pack_args(Q, cu_seqlens, ref_lens)
-    for name, t in (("K", K), ("V", V), ("Q", Q)):
-        _check_tensor(name, t, (L, H, d), Q.dtype, Q.device)
+    shape, index = Q.shape, Q.get_device()
     O = torch.empty_like(Q) if out is None else out
-    _check_tensor("out", O, (L, H, d), Q.dtype, Q.device)
-    lse = torch.empty((H, L), dtype=torch.float32, device=Q.device)
-    with torch.cuda.device(Q.device):
-        check(_native.lib().rswa_masked_forward_lse(
-            Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(), cu, refs, len(ref_lens), int(n),
-            H, d, _DT[Q.dtype], float(scale), _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0,
-            _stream_ptr(Q.device)))
+    for name, t in (("Q", Q), ("K", K), ("V", V), ("out", O)):
+        _check_like(name, t, Q, shape, index)
+    lse = Q.new_empty((H, L), dtype=torch.float32)
+    _call(index, _native.lib().rswa_masked_forward_lse, Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+          lse.data_ptr(), cu, refs, len(ref_lens), int(n), H, d, _DT[Q.dtype], float(scale),
+          _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0, _stream_ptr(Q.device))
     return O, lse
 
 
@@ -465,23 +487,29 @@ def masked_backward_varlen(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V
                            scale: float = 0.0, out=None, bidir_prefix: bool = False) -> tuple:
     """Gradient of masked_forward_varlen, as masked_backward: (dQ, dK, dV)."""
     L, H, d, cu, refs = _pack_args(Q, cu_seqlens, ref_lens)
-    grads = tuple(torch.empty_like(Q) for _ in range(3)) if out is None else tuple(out)
-    if len(grads) != 3:
+    shape, index = Q.shape, Q.get_device()
+    if out is None:
+        grads = torch.empty_like(Q), torch.empty_like(Q), torch.empty_like(Q)
+    elif len(out) == 3:
+        grads = tuple(out)
+    else:
         raise ValueError("out must be three tensors")
-    for name, t in (("dO", dO), ("Q", Q), ("K", K), ("V", V), ("O", O),
-                    ("out[0]", grads[0]), ("out[1]", grads[1]), ("out[2]", grads[2])):
-        _check_tensor(name, t, (L, H, d), Q.dtype, Q.device)
+    dQ, dK, dV = grads
+    for name, t in (("Q", Q), ("dO", dO), ("K", K), ("V", V), ("O", O)):
+        _check_like(name, t, Q, shape, index)
+    if out is not None:
+        for i, t in enumerate(grads):
+            _check_like(f"out[{i}]", t, Q, shape, index)
     _check_tensor("lse", lse, (H, L), torch.float32, Q.device)
     lib = _native.lib()
+    dt, docs, n = _DT[Q.dtype], len(ref_lens), int(n)
     flags = _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0
-    ws_bytes = lib.rswa_masked_backward_workspace_bytes(cu, refs, len(ref_lens), int(n), H, d, _DT[Q.dtype], flags)
+    ws_bytes = lib.rswa_masked_backward_workspace_bytes(cu, refs, docs, n, H, d, dt, flags)
     # 0 bytes: arguments that the call itself reports
-    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=Q.device)
-    with torch.cuda.device(Q.device):
-        check(lib.rswa_masked_backward(
-            dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(), lse.data_ptr(),
-            grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(), cu, refs, len(ref_lens), int(n), H, d,
-            _DT[Q.dtype], float(scale), flags, ws.data_ptr(), ws_bytes, _stream_ptr(Q.device)))
+    ws = Q.new_empty((max(ws_bytes, 16),), dtype=torch.uint8)
+    _call(index, lib.rswa_masked_backward, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
+          lse.data_ptr(), dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), cu, refs, docs, n, H, d, dt, float(scale),
+          flags, ws.data_ptr(), ws_bytes, _stream_ptr(Q.device))
     return grads
 
 
@@ -509,18 +537,19 @@ class Rotary:
                                              float(base), self._SCALINGS[scaling], float(factor),
                                              int(original_length)))
         self.mscale = self._plan.mscale
+        self._ref, self._apply = C.byref(self._plan), _native.lib().rswa_rotary_apply
 
-    def _stride(self, name: str, t: torch.Tensor, rows: int, like: torch.Tensor) -> int:
+    def _stride(self, name: str, t: torch.Tensor, rows: int, like: torch.Tensor, index: int) -> int:
         """Checks t ([rows, heads, d] with contiguous heads, a slice of wider
         rows or not) and returns its row stride in elements."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != self.d:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, heads, {self.d}]")
-        if t.dtype != like.dtype or t.device != like.device:
+        shape, s = t.shape, t.stride()
+        if len(shape) != 3 or shape[0] != rows or shape[2] != self.d:
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected [{rows}, heads, {self.d}]")
+        if t.dtype is not like.dtype or t.get_device() != index:
             raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {like.dtype} on {like.device}")
-        heads = t.shape[1]
-        s = t.stride()
+        heads = shape[1]
         if s[2] != 1 or (heads > 1 and s[1] != self.d):
             raise ValueError(f"{name} must have contiguous heads")
         return s[0] if rows > 1 else heads * self.d
@@ -536,35 +565,38 @@ class Rotary:
         themselves.  Returns Q's result, or the pair."""
         if not isinstance(Q, torch.Tensor):
             raise TypeError("Q must be a torch.Tensor")
-        if Q.device.type != "cuda":
+        if not Q.is_cuda:
             raise ValueError(f"Q is on {Q.device}, expected a CUDA device")
-        if Q.dtype not in _DT:
+        dt = _DT.get(Q.dtype)
+        if dt is None:
             raise ValueError(f"dtype {Q.dtype} not supported")
-        rows = Q.shape[0] if Q.dim() == 3 else 0
-        ins = (Q,) if K is None else (Q, K)
+        shape = Q.shape
+        rows = shape[0] if len(shape) == 3 else 0
         if out is None:
-            outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins)
+            q = torch.empty_like(Q, memory_format=torch.contiguous_format)
+            k = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
         else:
-            outs = (out,) if isinstance(out, torch.Tensor) else tuple(out)
-        if len(outs) != len(ins):
-            raise ValueError("out must hold one tensor for Q and one for K")
-        args = []
-        for name, t, o in zip(("Q", "K"), ins, outs):
-            sx = self._stride(name, t, rows, Q)
-            so = self._stride("out of " + name, o, rows, Q)
-            if o.shape != t.shape:
-                raise ValueError(f"out of {name} has shape {tuple(o.shape)}, expected {tuple(t.shape)}")
-            args += [t.data_ptr(), sx, t.shape[1], o.data_ptr(), so]
-        if K is None:
-            args += [None, 0, 0, None, 0]
+            q, k = (out, None) if K is None else out
+        index = Q.get_device()
         pos = None
         if positions is not None:
-            _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
+            if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.dim() == 1
+                    and positions.shape[0] == rows and positions.get_device() == index and positions.is_contiguous()):
+                _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
             pos = positions.data_ptr()
-        with torch.cuda.device(Q.device):
-            check(_native.lib().rswa_rotary_apply(self._plan, *args, pos, int(first), rows, _DT[Q.dtype],
-                                                  int(bool(inverse)), _stream_ptr(Q.device)))
-        return outs[0] if K is None else outs
+        sq, sqo = self._stride("Q", Q, rows, Q, index), self._stride("out of Q", q, rows, Q, index)
+        if q.shape != shape:
+            raise ValueError(f"out of Q has shape {tuple(q.shape)}, expected {tuple(shape)}")
+        if K is None:
+            keys = (None, 0, 0, None, 0)
+        else:
+            keys = (K.data_ptr(), self._stride("K", K, rows, Q, index), K.shape[1], k.data_ptr(),
+                    self._stride("out of K", k, rows, Q, index))
+            if k.shape != K.shape:
+                raise ValueError(f"out of K has shape {tuple(k.shape)}, expected {tuple(K.shape)}")
+        _call(index, self._apply, self._ref, Q.data_ptr(), sq, shape[1], q.data_ptr(), sqo, *keys, pos, int(first), rows,
+              dt, 1 if inverse else 0, _stream_ptr(Q.device))
+        return q if K is None else (q, k)
 
 
 def document_positions(cu_seqlens: Sequence[int], device=None) -> torch.Tensor:

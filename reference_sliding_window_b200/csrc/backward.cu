@@ -75,6 +75,7 @@ size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParams p) {
   constexpr int N = Vec16<T>::N, G = D / N;
+  launch_dependents();  // the items load their tiles while the statistics form
   const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
   const long long rh = idx / G;  // row * H + head
   const int e = (int)(idx % G) * N;
@@ -112,6 +113,7 @@ struct JoinParams {
 // Adds a split tile's partials in order.  One CTA per (tile, head).
 template <typename T>
 __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
+  dependency_wait();
   const BackwardParams& b = p.b;
   const BwdJoin w = p.join[blockIdx.x / b.H];
   const int h = blockIdx.x % b.H;
@@ -169,9 +171,9 @@ cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStr
   for (size_t w0 = 0; w0 < plan.joins.size(); w0 += kMaxJoin) {
     const int m = (int)std::min<size_t>(kMaxJoin, plan.joins.size() - w0);
     std::copy_n(plan.joins.begin() + w0, m, j.join);
-    if (elem == kF32) backward_join_kernel<float><<<m * p.H, 256, 0, stream>>>(j);
-    else backward_join_kernel<__nv_bfloat16><<<m * p.H, 256, 0, stream>>>(j);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(elem == kF32 ? backward_join_kernel<float> : backward_join_kernel<__nv_bfloat16>, m * p.H, 256, 0,
+                         stream, j);
+    if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }

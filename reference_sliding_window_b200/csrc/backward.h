@@ -91,7 +91,14 @@ struct BackwardParams {
 };
 
 constexpr int kBwdTileTc = 128, kBwdTileF32 = 64;
-constexpr int kBwdMaxWork = 960;  // work entries per launch (30 KB of kernel parameters)
+// Work entries per launch, which travel in the kernel's parameters: up to 30
+// KB, or 2 KB where that holds them (a launch with the large ones costs the
+// host about 2 us more).
+constexpr int kBwdMaxWork = 960, kBwdFewWork = 64;
+template <typename Common, int N>
+struct BwdLaunch : Common {
+  BwdWork work[N];  // heaviest first
+};
 
 size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_docs, int n, int H, int D, int elem,
                                 bool bidir);

@@ -24,6 +24,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 #include "backward.h"
 #include "common.cuh"
 
@@ -42,7 +44,6 @@ constexpr int smem_bytes() {
 struct F32Params {
   BackwardParams b;
   float scale_log2;
-  BwdWork work[kBwdMaxWork];
 };
 
 // Rows [row0, row0 + 64) of a packed [L][H][D] tensor's head h, asynchronously;
@@ -211,6 +212,7 @@ __device__ __forceinline__ void run_item(const F32Params& p, const BwdWork& w, i
   const int end = w.start + w.len;
   load_tile<D>(res0, DQ ? b.Q : b.K, w.start + own0, end, b.H, h);
   load_tile<D>(res1, DQ ? b.dO : b.V, w.start + own0, end, b.H, h);
+  dependency_wait();  // for the row statistics; Q, K, V and dO are older than the kernel that forms them
   // team 0: rows of Q, columns of K; team 1: rows of dO, columns of V
   const float* rows = DQ ? (team ? res1 : res0) : (team ? str1 : str0);
   const float* cols = DQ ? (team ? str1 : str0) : (team ? res1 : res0);
@@ -276,24 +278,38 @@ __device__ __forceinline__ void run_item(const F32Params& p, const BwdWork& w, i
                      gr, gc, g, t);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) backward_f32_kernel(const __grid_constant__ F32Params p) {
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads) backward_f32_kernel(const __grid_constant__ BwdLaunch<F32Params, N> p) {
   extern __shared__ __align__(16) float sm[];
+  launch_dependents();
   const BwdWork w = p.work[blockIdx.x / p.b.H];
   const int h = blockIdx.x % p.b.H;
   if (w.kind == kBwdDQ) run_item<D, true>(p, w, h, sm);
   else run_item<D, false>(p, w, h, sm);
 }
 
-template <int D>
-cudaError_t launch(const F32Params& p, int n_work, cudaStream_t stream) {
+template <int D, int N>
+cudaError_t launch(const F32Params& common, const BwdWork* work, int n_work, cudaStream_t stream) {
   static PerContextOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(backward_f32_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+    return cudaFuncSetAttribute(backward_f32_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
   });
   if (e != cudaSuccess) return e;
-  backward_f32_kernel<D><<<n_work * p.b.H, kThreads, smem_bytes<D>(), stream>>>(p);
-  return cudaGetLastError();
+  BwdLaunch<F32Params, N> p;
+  static_cast<F32Params&>(p) = common;
+  for (int w0 = 0; w0 < n_work; w0 += N) {
+    const int m = std::min(N, n_work - w0);
+    std::copy_n(work + w0, m, p.work);
+    e = launch_dependent(backward_f32_kernel<D, N>, m * p.b.H, kThreads, smem_bytes<D>(), stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch(const F32Params& p, const BwdWork* work, int n_work, cudaStream_t stream) {
+  return n_work <= kBwdFewWork ? launch<D, kBwdFewWork>(p, work, n_work, stream)
+                               : launch<D, kBwdMaxWork>(p, work, n_work, stream);
 }
 
 }  // namespace
@@ -302,13 +318,7 @@ cudaError_t launch_backward_f32(const BackwardParams& b, const BwdWork* work, in
   F32Params p;
   p.b = b;
   p.scale_log2 = b.scale * 1.4426950408889634f;
-  for (int w0 = 0; w0 < n_work; w0 += kBwdMaxWork) {
-    const int m = n_work - w0 < kBwdMaxWork ? n_work - w0 : kBwdMaxWork;
-    for (int i = 0; i < m; ++i) p.work[i] = work[w0 + i];
-    const cudaError_t e = b.D == 64 ? launch<64>(p, m, stream) : launch<128>(p, m, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return b.D == 64 ? launch<64>(p, work, n_work, stream) : launch<128>(p, work, n_work, stream);
 }
 
 }  // namespace rswa

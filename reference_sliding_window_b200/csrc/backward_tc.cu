@@ -51,7 +51,6 @@ struct BwdTcParams {
   CUtensorMap tmQ, tmK, tmV, tmG;  // packed [L][H][D] maps; G is dO
   BackwardParams b;
   float scale_log2;
-  BwdWork work[kBwdMaxWork];  // heaviest first
 };
 
 template <int D>
@@ -215,6 +214,9 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
   const bool bidir = p.b.bidir != 0;
+  // The row statistics come from the kernel before this one; Q, K, V and dO
+  // are older than that kernel's start.
+  dependency_wait();
   float nlse = 0.f, ndelta = 0.f;
   if (DQ && own < w.len) {
     const float2 st = p.b.stats[(size_t)c.h * p.b.stat_stride + w.start + own];
@@ -369,8 +371,9 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_constant__ BwdTcParams p) {
+template <int D, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    backward_tc_kernel(const __grid_constant__ BwdLaunch<BwdTcParams, N> p) {
   using C = Cfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -392,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
   const int nA = dq ? C::kAQ : C::kAKV;
   constexpr int nB = C::kB;
 
+  launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(B(kBarRes + s), 1);
@@ -535,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
   } else if (warp == 2) {
     // -------------------------------------------------- row statistics
     if (!dq) {
+      dependency_wait();
       for (int j = 0; j < nt; ++j) {
         const int s = j % nA;
         if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait_bounded(B(kBarAFree + s), ((j / nA) & 1) ^ 1))) break;
@@ -563,15 +568,28 @@ __global__ void __launch_bounds__(kThreads, 1) backward_tc_kernel(const __grid_c
                               : "memory");
 }
 
-template <int D>
-cudaError_t launch(const BwdTcParams& p, int n_work, cudaStream_t stream) {
+template <int D, int N>
+cudaError_t launch(const BwdTcParams& common, const BwdWork* work, int n_work, cudaStream_t stream) {
   static PerContextOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(backward_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmBytes);
+    return cudaFuncSetAttribute(backward_tc_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmBytes);
   });
   if (e != cudaSuccess) return e;
-  backward_tc_kernel<D><<<n_work * p.b.H, kThreads, Cfg<D>::kSmBytes, stream>>>(p);
-  return cudaGetLastError();
+  BwdLaunch<BwdTcParams, N> p;
+  static_cast<BwdTcParams&>(p) = common;
+  for (int w0 = 0; w0 < n_work; w0 += N) {
+    const int m = std::min(N, n_work - w0);
+    std::copy_n(work + w0, m, p.work);
+    e = launch_dependent(backward_tc_kernel<D, N>, m * p.b.H, kThreads, Cfg<D>::kSmBytes, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t launch(const BwdTcParams& p, const BwdWork* work, int n_work, cudaStream_t stream) {
+  return n_work <= kBwdFewWork ? launch<D, kBwdFewWork>(p, work, n_work, stream)
+                               : launch<D, kBwdMaxWork>(p, work, n_work, stream);
 }
 
 }  // namespace
@@ -585,13 +603,7 @@ cudaError_t launch_backward_tc(const BackwardParams& b, const BwdWork* work, int
     return cudaErrorInvalidValue;
   p.b = b;
   p.scale_log2 = b.scale * 1.4426950408889634f;
-  for (int w0 = 0; w0 < n_work; w0 += kBwdMaxWork) {
-    const int m = std::min(kBwdMaxWork, n_work - w0);
-    std::copy_n(work + w0, m, p.work);
-    const cudaError_t e = b.D == 64 ? launch<64>(p, m, stream) : launch<128>(p, m, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return b.D == 64 ? launch<64>(p, work, n_work, stream) : launch<128>(p, work, n_work, stream);
 }
 
 }  // namespace rswa

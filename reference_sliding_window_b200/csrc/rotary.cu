@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   const long long rg = idx / units;
   const int g = (int)(rg % groups);
   const long long row = rg / groups;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  dependency_wait();
   if (row >= p.rows) return;
   const int dim = p.plan.dim, half = dim / 2;
   const bool turns = u * kPairs < half;

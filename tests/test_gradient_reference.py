@@ -11,7 +11,8 @@ import pytest
 import torch
 
 import oracle
-from reference_sliding_window_b200 import Rotary, RSWAError, _native, document_positions, synth
+from reference_sliding_window_b200 import (Rotary, RSWAError, _native, document_positions, masked_attention,
+                                           masked_backward, masked_forward, synth)
 from tests import gradients
 
 
@@ -100,6 +101,16 @@ def test_rotary_plan_refusals():
         Rotary(64, scaling="other")
     with pytest.raises(ValueError, match="CUDA"):
         Rotary(64).apply(torch.zeros(3, 2, 64))
+
+
+def test_host_tensors_are_refused():
+    x, lse = torch.zeros(4, 1, 64), torch.zeros(1, 4)
+    with pytest.raises(ValueError, match="CUDA"):
+        masked_backward(x, x, x, x, x, lse, L_m=2, n=1)
+    with pytest.raises(ValueError, match="CUDA"):
+        masked_forward(x, x, x, L_m=2, n=1, return_lse=True)
+    with pytest.raises(ValueError, match="CUDA"):
+        masked_attention(x, x, x, L_m=2, n=1)
 
 
 def test_document_positions():
