@@ -16,8 +16,8 @@
 //   read from TMEM.
 // * Warp 0 streams tiles with TMA (128-byte swizzle) through two rings, warp
 //   1 issues the MMAs, warp 2 stages the row statistics (dK, dV items, where
-//   they vary along a thread's columns), warps 4-11 are the softmax: two
-//   groups of 128 threads, one thread per TMEM lane and half of its 128
+//   they vary along a thread's columns), warps 4-19 are the softmax: four
+//   groups of 128 threads, one thread per TMEM lane and a quarter of its 128
 //   columns.
 // * Issue order of a dK, dV item, two score regions X, Y taking turns: S(i)
 //   in one, dP(i) in the other; while the softmax forms P(i) the tensor pipe
@@ -42,9 +42,10 @@ namespace rswa {
 namespace tc {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kSoftmaxWarp = 4;
-constexpr int kSoftmaxThreads = 256;
+constexpr int kSoftmaxThreads = 512;
+constexpr int kCols = 32;  // score columns of a softmax thread
 constexpr int kTmemCols = 512;
 
 struct BwdTcParams {
@@ -57,24 +58,28 @@ template <int D>
 struct Cfg {
   static constexpr int kBoxes = D / kBox;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
-  // ring A: K tiles (dQ items: read by S and, two tiles later, by dQ) or Q tiles; ring B: V or dO tiles
-  static constexpr int kAQ = D == 128 ? 3 : 4, kAKV = D == 128 ? 2 : 4, kB = D == 128 ? 2 : 4;
+  // Ring A: K tiles (dQ items) or Q tiles, read by S and again, a tile's
+  // softmax later, by dQ or dK; ring B: V or dO tiles.  Two stages of ring A are
+  // too few: the tile after next then waits for its load (a dK, dV tile pair
+  // took 4560 cycles with two stages).
+  static constexpr int kA = D == 128 ? 3 : 4, kB = D == 128 ? 2 : 4;
   static constexpr int kSmRes = 0;
   static constexpr int kSmA = kSmRes + 2 * kTileBytes;
-  static constexpr int kSmB = kSmA + kAQ * kTileBytes;
-  // statistics of the streamed query tiles (dK, dV items): where D = 128, in
-  // the third stage of ring A, which these items do not use
-  static constexpr int kSmStats = D == 128 ? kSmA + 2 * kTileBytes : kSmB + kB * kTileBytes;
-  static constexpr int kSmBar = kSmB + kB * kTileBytes + (D == 128 ? 0 : kAKV * 1024);
-  static constexpr int kSmBytes = kSmBar + 512 + 1024;  // + slack for 1024-byte alignment
+  static constexpr int kSmB = kSmA + kA * kTileBytes;
+  // statistics of two streamed query tiles (dK, dV items)
+  static constexpr int kSmStats = kSmB + kB * kTileBytes;
+  static constexpr int kSmBar = kSmStats + 2 * 1024;
+  static constexpr int kSmBytes = kSmBar + 512;
 };
+static_assert(Cfg<128>::kSmBytes <= 232448 && Cfg<64>::kSmBytes <= 232448, "shared memory of an SM");
 
 // A wait names one of a barrier's two phases, so a barrier's next phase but one
 // must not complete while a waiter has still to see this one.  S, P and dS run
 // up to two tiles ahead of the MMA thread's or the softmax's waits (S(j+1) is
 // issued before P(j) is awaited; a dQ item's dS(j+1) needs nothing that follows
 // the wait for dS(j)) and take two barriers in turn; everything else is
-// ordered by the ring's or the region's next use.
+// ordered by the ring's or the region's next use.  (Warp 2's wait for dS(j)
+// comes before it stages the statistics that dS(j+2) needs.)
 enum : int {
   kBarRes = 0,      // 2
   kBarAFull = 2,    // 4
@@ -85,8 +90,8 @@ enum : int {
   kBarP = 20,       // 2
   kBarDS = 22,      // 2
   kBarDP = 24, kBarDPRead = 25, kBarFinal = 26,
-  kBarStats = 27,   // 4
-  kSlotTmem = 31, kSlotAbort = 32
+  kBarStats = 27,   // 2
+  kSlotTmem = 29, kSlotAbort = 30
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -134,14 +139,14 @@ __device__ __forceinline__ void mma_scores(int lead, uint32_t tmem_d, uint32_t a
   }
 }
 
-// D (TMEM, 128 x D) += A B: A 128 x 128 bf16 pairs in TMEM, its columns [0,
-// 64) at tmem_a and [64, 128) 64 TMEM columns on; B a tile's rows.
+// D (TMEM, 128 x D) += A B: A 128 x 128 bf16 pairs in TMEM, 32 columns of it at
+// tmem_a, the next 32 kCols TMEM columns on, ...; B a tile's rows.
 template <int D>
 __device__ __forceinline__ void mma_grad(int lead, uint32_t tmem_d, uint32_t tmem_a, uint32_t b, bool acc) {
   const uint64_t db = smem_desc(b, kBoxBytes, 1024);
 #pragma unroll
   for (int kk = 0; kk < kTile / 16; ++kk)
-    mma_ts(lead, tmem_d, tmem_a + (kk >> 2) * 64 + (kk & 3) * 8, db + ((kk * 2048) >> 4), idesc(D, true),
+    mma_ts(lead, tmem_d, tmem_a + (kk >> 1) * kCols + (kk & 1) * 8, db + ((kk * 2048) >> 4), idesc(D, true),
            kk > 0 ? 1u : acc);
 }
 
@@ -173,10 +178,10 @@ __device__ __forceinline__ void addmul2(float& p0, float& p1, float x0, float x1
   asm("mov.b64 {%0, %1}, %2;" : "=f"(p0), "=f"(p1) : "l"(p));
 }
 
-// Bits [lo, hi) of 64.
-__device__ __forceinline__ unsigned long long bit_range(int lo, int hi) {
-  const unsigned long long below_hi = hi <= 0 ? 0ull : hi >= 64 ? ~0ull : (1ull << hi) - 1;
-  const unsigned long long below_lo = lo <= 0 ? 0ull : lo >= 64 ? ~0ull : (1ull << lo) - 1;
+// Bits [lo, hi) of 32.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
+  const uint32_t below_hi = hi <= 0 ? 0u : hi >= 32 ? ~0u : (1u << hi) - 1;
+  const uint32_t below_lo = lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1;
   return below_hi & ~below_lo;
 }
 // N elements zeroed (whatever they hold, NaN included) where their bit is clear.
@@ -185,6 +190,11 @@ __device__ __forceinline__ void keep(float* x, uint32_t bits) {
 #pragma unroll
   for (int e = 0; e < N; ++e)
     x[e] = __uint_as_float(__float_as_uint(x[e]) & (uint32_t)((int)(bits << (31 - e)) >> 31));
+}
+
+// A bounded wait that ends early once the CTA has given up.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, int phase, volatile int* abort) {
+  return mbar_try_wait(bar, phase & 1) || (!*abort && mbar_wait_bounded(bar, phase & 1));
 }
 
 struct Ctx {
@@ -202,14 +212,14 @@ struct Ctx {
 template <int D, bool DQ>
 __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   using C = Cfg<D>;
-  constexpr int nA = DQ ? C::kAQ : C::kAKV, nB = C::kB;
+  constexpr int nA = C::kA, nB = C::kB;
   const BwdTcParams& p = c.p;
   const BwdWork& w = c.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = (warp - kSoftmaxWarp) >> 2;  // column half
+  const int g = (warp - kSoftmaxWarp) >> 2;  // column quarter
   const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
   const int r = quarter * 32 + lane;
-  const int c0 = 64 * g;
+  const int c0 = kCols * g;
   const int own = w.tile * kTile + r;        // local row: the thread's query (DQ) or key
   const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
@@ -227,7 +237,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   // After a timed-out wait a thread stops waiting but keeps arriving, so
   // the MMA thread is not left waiting on it; its rows are written as NaN.
   auto wait = [&](int slot, int phase) {
-    if (ok && (*c.abort || !mbar_wait_bounded(c.bar0 + 8u * slot, phase & 1))) ok = false;
+    if (ok && !wait_phase(c.bar0 + 8u * slot, phase, c.abort)) ok = false;
   };
   // A warp's arrival, once all of its lanes are there: an arrival per lane
   // costs an operation on the barrier's word each.
@@ -243,7 +253,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     // whether every pair of the tiles is visible; otherwise the thread's
     // visible columns
     bool full;
-    unsigned long long vis = ~0ull;
+    uint32_t vis = ~0u;
     if (DQ) {
       const int q0 = w.tile * kTile;
       full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
@@ -263,16 +273,15 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
         vis = bit_range((own < w.ref && bidir ? 0 : own) - o0 - c0,
                         (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - o0 - c0);
     }
-    const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it % nA) * 2 * kTile + c0;
-    if (!DQ) wait(kBarStats + it % nA, it / nA);
+    const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it & 1) * 2 * kTile + c0;
+    if (!DQ) wait(kBarStats + (it & 1), it >> 1);
     wait(kBarS + (it & 1), it >> 1);
     tc_fence_after();
-    float x[64];
+    float x[kCols];
     tmem_ld32(tS, x);
-    tmem_ld32(tS + 32, x + 32);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 64; e += 4) {
+    for (int e = 0; e < kCols; e += 4) {
       float4 l4 = make_float4(nlse, nlse, nlse, nlse);
       if (!DQ) l4 = *reinterpret_cast<const float4*>(st + e);
       fma2(x[e], x[e + 1], sl2, l4.x, l4.y);
@@ -281,8 +290,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
       for (int i = 0; i < 4; ++i) x[e + i] = ex2(x[e + i]);
     }
     if (!full) {
-      keep<32>(x, (uint32_t)vis);
-      keep<32>(x + 32, (uint32_t)(vis >> 32));
+      keep<kCols>(x, vis);
       // rows of the streamed tiles past the document's end
       const int valid = w.len - o0;
       if (valid < kTile) {
@@ -297,41 +305,34 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
       }
     }
     if (!DQ) {
+      uint32_t pk[kCols / 2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]);
-        tmem_st_words(tS + 16 * q, pk);
-      }
+      for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+      tmem_st_words(tS, pk);
       tmem_wait_st();
       tc_fence_before();
       arrive(kBarP + (it & 1));
     }
     wait(kBarDP, it);
     tc_fence_after();
-    float dp[64];
+    float dp[kCols];
     tmem_ld32(tP, dp);
-    tmem_ld32(tP + 32, dp + 32);
     tmem_wait_ld();
     tc_fence_before();
     arrive(kBarDPRead);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-      for (int e = 32 * q; e < 32 * q + 32; e += 4) {
-        float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-        if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
-        addmul2(x[e], x[e + 1], dp[e], dp[e + 1], d4.x, d4.y);
-        addmul2(x[e + 2], x[e + 3], dp[e + 2], dp[e + 3], d4.z, d4.w);
-      }
-      // a masked weight of 0 times a NaN of another document's row
-      if (!full) keep<32>(x + 32 * q, (uint32_t)(vis >> (32 * q)));
-      uint32_t pk[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]);
-      tmem_st_words((DQ ? tS : tS + 32) + 16 * q, pk);
+    for (int e = 0; e < kCols; e += 4) {
+      float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
+      if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
+      addmul2(x[e], x[e + 1], dp[e], dp[e + 1], d4.x, d4.y);
+      addmul2(x[e + 2], x[e + 3], dp[e + 2], dp[e + 3], d4.z, d4.w);
     }
+    // a masked weight of 0 times a NaN of another document's row
+    if (!full) keep<kCols>(x, vis);
+    uint32_t pk[kCols / 2];
+#pragma unroll
+    for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+    tmem_st_words(DQ ? tS : tS + kCols / 2, pk);
     tmem_wait_st();
     tc_fence_before();
     arrive(kBarDS + (it & 1));
@@ -341,31 +342,31 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   tc_fence_after();
   if (!ok) *c.abort = 1;
   const bool good = ok && !*c.abort;
-  // dQ: each group half of the columns; dK, dV: group 0 dV, group 1 dK
-  constexpr int kCols = DQ ? D / 2 : D;
-  const int col0 = DQ ? g * kCols : 0;
-  const uint32_t src = c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 + col0 : 256 + 128 * g);
+  // dQ: each group a quarter of the columns; dK, dV: groups 0, 1 halves of dV, 2, 3 of dK
+  constexpr int kMine = DQ ? D / 4 : D / 2;
+  const int col0 = (DQ ? g : g & 1) * kMine, which = DQ ? 0 : g >> 1;
+  const uint32_t src = c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col0;
   const int H = p.b.H;
   float* part = w.part < 0 ? nullptr
-                           : p.b.partials + (((size_t)w.part * H + c.h) * 2 + (DQ ? 0 : g)) * kTile * D + r * D + col0;
-  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : g == 0 ? p.b.dV : p.b.dK) +
+                           : p.b.partials + (((size_t)w.part * H + c.h) * 2 + which) * kTile * D + r * D + col0;
+  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
                         ((size_t)(w.start + own) * H + c.h) * D + col0;
-  const float mul = !good ? __int_as_float(0x7fc00000) : part || (!DQ && g == 0) ? 1.f : p.b.scale;
+  const float mul = !good ? __int_as_float(0x7fc00000) : part || (!DQ && which == 0) ? 1.f : p.b.scale;
 #pragma unroll 1
-  for (int k = 0; k < kCols; k += 32) {
-    float o[32];
-    tmem_ld32(src + k, o);
+  for (int k = 0; k < kMine; k += 16) {
+    float o[16];
+    tmem_ld16(src + k, o);
     tmem_wait_ld();
     if (own < w.len) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] *= mul;
+      for (int e = 0; e < 16; ++e) o[e] *= mul;
       if (part) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
+        for (int e = 0; e < 16; e += 4)
           *reinterpret_cast<float4*>(part + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       } else {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) *reinterpret_cast<uint4*>(grad + k + e) = pack16<__nv_bfloat16>(o + e);
+        for (int e = 0; e < 16; e += 8) *reinterpret_cast<uint4*>(grad + k + e) = pack16<__nv_bfloat16>(o + e);
       }
     }
   }
@@ -375,8 +376,7 @@ template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     backward_tc_kernel(const __grid_constant__ BwdLaunch<BwdTcParams, N> p) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's period)
   const uint32_t sbase = smem_u32(smem);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kSmBar);
   const uint32_t bar0 = smem_u32(bars);
@@ -392,14 +392,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const BwdTiles seq = dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir)
                           : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir);
   const int nt = w.hi - w.lo;
-  const int nA = dq ? C::kAQ : C::kAKV;
-  constexpr int nB = C::kB;
+  constexpr int nA = C::kA, nB = C::kB;
 
   launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(B(kBarRes + s), 1);
       mbar_init(B(kBarS + s), 1);
+      mbar_init(B(kBarStats + s), 1);
       mbar_init(B(kBarP + s), kSoftmaxThreads / 32);
       mbar_init(B(kBarDS + s), kSoftmaxThreads / 32);
     }
@@ -408,12 +408,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(B(kBarAFree + s), 1);
       mbar_init(B(kBarBFull + s), 1);
       mbar_init(B(kBarBFree + s), 1);
-      mbar_init(B(kBarStats + s), 1);
     }
     mbar_init(B(kBarDP), 1);
     mbar_init(B(kBarDPRead), kSoftmaxThreads / 32);
     mbar_init(B(kBarFinal), 1);
-    *s_abort = 0;
+    *s_abort = (sbase & 1023) != 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -467,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lead = lane == 0;
       // (every lane of the warp answers the same)
       auto wait = [&](int slot, int phase) {
-        return __all_sync(0xffffffffu, !*s_abort && mbar_wait_bounded(B(slot), phase & 1)) != 0;
+        return __all_sync(0xffffffffu, wait_phase(B(slot), phase, s_abort)) != 0;
       };
       auto tileA = [&](int j) { return smA + (j % nA) * C::kTileBytes; };
       auto tileB = [&](int j) { return smB + (j % nB) * C::kTileBytes; };
@@ -526,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + 32, tileA(j), j > 0);
+          mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + kCols / 2, tileA(j), j > 0);
           commit(lead, B(kBarAFree + j % nA));
           if (j + 1 < nt) ok = dprob(j + 1);
         }
@@ -541,8 +540,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!dq) {
       dependency_wait();
       for (int j = 0; j < nt; ++j) {
-        const int s = j % nA;
-        if (!__all_sync(0xffffffffu, !*s_abort && mbar_wait_bounded(B(kBarAFree + s), ((j / nA) & 1) ^ 1))) break;
+        const int s = j & 1;
+        // the softmax has read the statistics of tile j - 2 once its dS is there
+        const bool free = j < 2 || (!*s_abort && mbar_wait_bounded(B(kBarDS + s), ((j - 2) >> 1) & 1));
+        if (!__all_sync(0xffffffffu, free)) break;
         // rows past the document's end are another's, or padding of the array
         const float2* src = p.b.stats + (size_t)h * p.b.stat_stride + w.start + seq.at(w.lo + j) * kTile;
         float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
