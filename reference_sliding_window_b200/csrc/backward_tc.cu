@@ -20,9 +20,10 @@
 //   groups of 128 threads, one thread per TMEM lane and a quarter of its 128
 //   columns.
 // * Issue order of a dK, dV item, two score regions X, Y taking turns: S(i)
-//   in one, dP(i) in the other; while the softmax forms P(i) the tensor pipe
-//   runs dK(i-1) and dP(i), while it forms dS(i) it runs S(i+1), over the dP(i)
-//   just read, and dV(i).  A dQ item has two regions for S and one for dP, so
+//   in one, dP(i) in the other, then dV(i), which runs while the softmax reads
+//   dP(i), S(i+1) over the dP(i) just read, dK(i) and dP(i+1), under which it forms
+//   P(i+1).  (S(i+1) before dV(i) left the tensor pipe idle while dP(i) was read:
+//   4100 cycles a tile pair.)  A dQ item has two regions for S and one for dP, so
 //   S runs two tiles ahead.
 // * P and dS are rounded to bf16 for the products, as the tensor cores take
 //   them (relative error 2^-8 at most on each term of sums of independent
@@ -150,12 +151,39 @@ __device__ __forceinline__ void mma_grad(int lead, uint32_t tmem_d, uint32_t tme
            kk > 0 ? 1u : acc);
 }
 
-// 16 words of bf16 pairs into 16 TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_st_words(uint32_t taddr, const uint32_t* w) {
-  float v[16];
+// A warp's 32 lanes x 32 TMEM columns as MMA fragments: with g = lane / 4 and t
+// = lane % 4, v[16 h + 4 k + r] is TMEM lane 16 h + 8 (r / 2) + g, column 8 k +
+// 2 t + r % 2.  A thread then holds 4 rows of 8 columns, so a value that
+// belongs to a column is read from shared memory once for 4 elements (one row
+// of 32 columns a thread read 128 bits for 4 elements, and those reads,
+// 1024 cycles a tile pair, delayed the MMAs' own).
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
+  uint32_t r[32];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i]);
-  tmem_st16(taddr, v);
+  for (int h = 0; h < 2; ++h)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[16 * h]), "=r"(r[16 * h + 1]), "=r"(r[16 * h + 2]), "=r"(r[16 * h + 3]), "=r"(r[16 * h + 4]),
+          "=r"(r[16 * h + 5]), "=r"(r[16 * h + 6]), "=r"(r[16 * h + 7]), "=r"(r[16 * h + 8]), "=r"(r[16 * h + 9]),
+          "=r"(r[16 * h + 10]), "=r"(r[16 * h + 11]), "=r"(r[16 * h + 12]), "=r"(r[16 * h + 13]),
+          "=r"(r[16 * h + 14]), "=r"(r[16 * h + 15])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16)));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// The same elements rounded to bf16 pairs, into 16 columns of the 32 lanes.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const float* v) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                     taddr + ((uint32_t)(16 * h) << 16)),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  }
 }
 
 // Two floats at a time (the same roundings per element).
@@ -184,12 +212,18 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_lo = lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1;
   return below_hi & ~below_lo;
 }
-// N elements zeroed (whatever they hold, NaN included) where their bit is clear.
-template <int N>
-__device__ __forceinline__ void keep(float* x, uint32_t bits) {
+// Fragment elements zeroed (whatever they hold, NaN included) where the bit of
+// their column, vis[i] for row 8 i + g, is clear.
+__device__ __forceinline__ void keep(float* x, const uint32_t* vis, int t) {
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    x[e] = __uint_as_float(__float_as_uint(x[e]) & (uint32_t)((int)(bits << (31 - e)) >> 31));
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bits = vis[i] >> (2 * t);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float& y = x[16 * (i >> 1) + 2 * (i & 1) + 4 * (e >> 1) + (e & 1)];
+      y = __uint_as_float(__float_as_uint(y) & (uint32_t)((int)(bits << (31 - 8 * (e >> 1) - (e & 1))) >> 31));
+    }
+  }
 }
 
 // A bounded wait that ends early once the CTA has given up.
@@ -218,20 +252,24 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = (warp - kSoftmaxWarp) >> 2;  // column quarter
   const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
-  const int r = quarter * 32 + lane;
+  const int fg = lane >> 2, ft = lane & 3;   // the fragments' row and column pair
   const int c0 = kCols * g;
-  const int own = w.tile * kTile + r;        // local row: the thread's query (DQ) or key
+  const int own0 = w.tile * kTile + quarter * 32 + fg;  // the thread's local rows own0 + 8 i: queries (DQ) or keys
   const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
   const bool bidir = p.b.bidir != 0;
   // The row statistics come from the kernel before this one; Q, K, V and dO
   // are older than that kernel's start.
   dependency_wait();
-  float nlse = 0.f, ndelta = 0.f;
-  if (DQ && own < w.len) {
-    const float2 st = p.b.stats[(size_t)c.h * p.b.stat_stride + w.start + own];
-    nlse = st.x;
-    ndelta = st.y;
+  float nlse[4], ndelta[4];
+  if (DQ) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)c.h * p.b.stat_stride + w.start + own0 + 8 * i]
+                                             : make_float2(0.f, 0.f);
+      nlse[i] = st.x;
+      ndelta[i] = st.y;
+    }
   }
   bool ok = true;
   // After a timed-out wait a thread stops waiting but keeps arriving, so
@@ -250,47 +288,55 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     const int o0 = c.seq.at(j) * kTile;  // first local row of the streamed tile
     const uint32_t tS = base + (DQ ? (it & 1) * 256 : (it & 1) * 128);
     const uint32_t tP = base + (DQ ? 128 : ((it & 1) ^ 1) * 128);
-    // whether every pair of the tiles is visible; otherwise the thread's
-    // visible columns
+    // whether every pair of the tiles is visible; otherwise the visible columns
+    // of the thread's rows
     bool full;
-    uint32_t vis = ~0u;
+    uint32_t vis[4];
     if (DQ) {
       const int q0 = w.tile * kTile;
       full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
       if (!full) {
-        if (own < w.ref) {
-          vis = bit_range(0, (bidir ? w.ref : own + 1) - o0 - c0);
-        } else {
-          vis = bit_range(0, w.ref - o0 - c0) |
-                bit_range(max(w.ref, own - p.b.n + 1) - o0 - c0, own + 1 - o0 - c0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int own = own0 + 8 * i, x0 = o0 + c0;
+          vis[i] = own < w.ref ? bit_range(0, (bidir ? w.ref : own + 1) - x0)
+                               : bit_range(0, w.ref - x0) | bit_range(max(w.ref, own - p.b.n + 1) - x0, own + 1 - x0);
         }
       }
     } else {
       const int k0 = w.tile * kTile, last = o0 + kTile - 1;
       full = last < w.len && ((k0 + kTile <= w.ref && (bidir || k0 + kTile - 1 <= o0)) ||
                               (k0 + kTile - 1 <= o0 && (long long)k0 + p.b.n > last));
-      if (!full)
-        vis = bit_range((own < w.ref && bidir ? 0 : own) - o0 - c0,
-                        (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - o0 - c0);
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int own = own0 + 8 * i, x0 = o0 + c0;
+          vis[i] = bit_range((own < w.ref && bidir ? 0 : own) - x0,
+                             (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - x0);
+        }
+      }
     }
     const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it & 1) * 2 * kTile + c0;
     if (!DQ) wait(kBarStats + (it & 1), it >> 1);
     wait(kBarS + (it & 1), it >> 1);
     tc_fence_after();
     float x[kCols];
-    tmem_ld32(tS, x);
+    tmem_ld_frag(tS, x);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < kCols; e += 4) {
-      float4 l4 = make_float4(nlse, nlse, nlse, nlse);
-      if (!DQ) l4 = *reinterpret_cast<const float4*>(st + e);
-      fma2(x[e], x[e + 1], sl2, l4.x, l4.y);
-      fma2(x[e + 2], x[e + 3], sl2, l4.z, l4.w);
+    for (int k = 0; k < 4; ++k) {
+      float2 l = make_float2(0.f, 0.f);
+      if (!DQ) l = *reinterpret_cast<const float2*>(st + 8 * k + 2 * ft);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[e + i] = ex2(x[e + i]);
+      for (int i = 0; i < 4; ++i) {
+        float* y = x + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+        fma2(y[0], y[1], sl2, DQ ? nlse[i] : l.x, DQ ? nlse[i] : l.y);
+        y[0] = ex2(y[0]);
+        y[1] = ex2(y[1]);
+      }
     }
     if (!full) {
-      keep<kCols>(x, vis);
+      keep(x, vis, ft);
       // rows of the streamed tiles past the document's end
       const int valid = w.len - o0;
       if (valid < kTile) {
@@ -305,10 +351,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
       }
     }
     if (!DQ) {
-      uint32_t pk[kCols / 2];
-#pragma unroll
-      for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-      tmem_st_words(tS, pk);
+      tmem_st_frag(tS, x);
       tmem_wait_st();
       tc_fence_before();
       arrive(kBarP + (it & 1));
@@ -316,23 +359,23 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     wait(kBarDP, it);
     tc_fence_after();
     float dp[kCols];
-    tmem_ld32(tP, dp);
+    tmem_ld_frag(tP, dp);
     tmem_wait_ld();
     tc_fence_before();
     arrive(kBarDPRead);
 #pragma unroll
-    for (int e = 0; e < kCols; e += 4) {
-      float4 d4 = make_float4(ndelta, ndelta, ndelta, ndelta);
-      if (!DQ) d4 = *reinterpret_cast<const float4*>(st + kTile + e);
-      addmul2(x[e], x[e + 1], dp[e], dp[e + 1], d4.x, d4.y);
-      addmul2(x[e + 2], x[e + 3], dp[e + 2], dp[e + 3], d4.z, d4.w);
+    for (int k = 0; k < 4; ++k) {
+      float2 d = make_float2(0.f, 0.f);
+      if (!DQ) d = *reinterpret_cast<const float2*>(st + kTile + 8 * k + 2 * ft);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+        addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
+      }
     }
     // a masked weight of 0 times a NaN of another document's row
-    if (!full) keep<kCols>(x, vis);
-    uint32_t pk[kCols / 2];
-#pragma unroll
-    for (int e = 0; e < kCols / 2; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
-    tmem_st_words(DQ ? tS : tS + kCols / 2, pk);
+    if (!full) keep(x, vis, ft);
+    tmem_st_frag(DQ ? tS : tS + kCols / 2, x);
     tmem_wait_st();
     tc_fence_before();
     arrive(kBarDS + (it & 1));
@@ -344,6 +387,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   const bool good = ok && !*c.abort;
   // dQ: each group a quarter of the columns; dK, dV: groups 0, 1 halves of dV, 2, 3 of dK
   constexpr int kMine = DQ ? D / 4 : D / 2;
+  const int r = quarter * 32 + lane, own = w.tile * kTile + r;  // one row per thread here
   const int col0 = (DQ ? g : g & 1) * kMine, which = DQ ? 0 : g >> 1;
   const uint32_t src = c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col0;
   const int H = p.b.H;
@@ -516,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0);
         for (int j = 0; j < nt && ok; ++j) {
-          if (j + 1 < nt) ok = wait(kBarDPRead, j) && scores(j + 1);
-          ok = ok && wait(kBarP + (j & 1), j >> 1);
+          ok = wait(kBarP + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           mma_grad<D>(lead, dV, tmem + (j & 1) * 128, tileB(j), j > 0);
           commit(lead, B(kBarBFree + j % nB));
-          ok = wait(kBarDS + (j & 1), j >> 1);
+          if (j + 1 < nt) ok = wait(kBarDPRead, j) && scores(j + 1);
+          ok = ok && wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
           mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + kCols / 2, tileA(j), j > 0);
