@@ -12,8 +12,11 @@
 //   and dS, bf16 pairs written over S's columns, are at once the A operands
 //   (read from TMEM) of dV += P^T dO and dK += dS^T Q, whose B operands are
 //   the streamed tiles themselves.
-// * A dQ item keeps Q and dO, streams K and V, and adds dQ += dS K with dS
-//   read from TMEM.
+// * A dQ item keeps its Q and dO rows in TMEM, as the A operands of S = Q K^T and
+//   dP = dO V^T, streams K and V, and adds dQ += dS K with dS written over dP.
+//   An MMA that reads both operands from shared memory takes 90 cycles
+//   instead of 64 (16 KB of operands at 128 bytes a cycle, and the ring's
+//   writes); with A in TMEM it takes 68.  A dK, dV item has no TMEM left for it.
 // * Warp 0 streams tiles with TMA (128-byte swizzle) through two rings, warp
 //   1 issues the MMAs, warp 2 stages the row statistics (dK, dV items, where
 //   they vary along a thread's columns), warps 4-19 are the softmax: four
@@ -23,8 +26,8 @@
 //   in one, dP(i) in the other, then dV(i), which runs while the softmax reads
 //   dP(i), S(i+1) over the dP(i) just read, dK(i) and dP(i+1), under which it forms
 //   P(i+1).  (S(i+1) before dV(i) left the tensor pipe idle while dP(i) was read:
-//   4100 cycles a tile pair.)  A dQ item has two regions for S and one for dP, so
-//   S runs two tiles ahead.
+//   4100 cycles a tile pair.)  A dQ item: S(i+1) as soon as S(i) is read, dQ(i),
+//   dP(i+1) over the dS(i) just used.
 // * P and dS are rounded to bf16 for the products, as the tensor cores take
 //   them (relative error 2^-8 at most on each term of sums of independent
 //   terms); dS is formed from the float32 P.
@@ -48,6 +51,7 @@ constexpr int kSoftmaxWarp = 4;
 constexpr int kSoftmaxThreads = 512;
 constexpr int kCols = 32;  // score columns of a softmax thread
 constexpr int kTmemCols = 512;
+constexpr uint32_t kColA = 256;  // dQ items: the rows of Q, then of dO, bf16 pairs
 
 struct BwdTcParams {
   CUtensorMap tmQ, tmK, tmV, tmG;  // packed [L][H][D] maps; G is dO
@@ -75,14 +79,12 @@ struct Cfg {
 static_assert(Cfg<128>::kSmBytes <= 232448 && Cfg<64>::kSmBytes <= 232448, "shared memory of an SM");
 
 // A wait names one of a barrier's two phases, so a barrier's next phase but one
-// must not complete while a waiter has still to see this one.  S, P and dS run
-// up to two tiles ahead of the MMA thread's or the softmax's waits (S(j+1) is
-// issued before P(j) is awaited; a dQ item's dS(j+1) needs nothing that follows
-// the wait for dS(j)) and take two barriers in turn; everything else is
-// ordered by the ring's or the region's next use.  (Warp 2's wait for dS(j)
-// comes before it stages the statistics that dS(j+2) needs.)
+// must not complete while a waiter has still to see this one.  S, P and dS take
+// two barriers in turn; everything else is ordered by the ring's or the region's
+// next use.  (Warp 2's wait for dS(j) comes before it stages the statistics that
+// dS(j+2) needs.)
 enum : int {
-  kBarRes = 0,      // 2
+  kBarRes = 0,      // 2: the item's own tiles; dQ items: both have landed, both are in TMEM
   kBarAFull = 2,    // 4
   kBarAFree = 6,    // 4
   kBarBFull = 10,   // 4
@@ -90,7 +92,9 @@ enum : int {
   kBarS = 18,       // 2
   kBarP = 20,       // 2
   kBarDS = 22,      // 2
-  kBarDP = 24, kBarDPRead = 25, kBarFinal = 26,
+  kBarDP = 24,
+  kBarRead = 25,    // dK, dV items: dP is read; dQ items: S is
+  kBarFinal = 26,
   kBarStats = 27,   // 2
   kSlotTmem = 29, kSlotAbort = 30
 };
@@ -138,6 +142,16 @@ __device__ __forceinline__ void mma_scores(int lead, uint32_t tmem_d, uint32_t a
     const uint32_t off = ((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4;
     mma_ss(lead, tmem_d, da + off, db + off, idesc(kTile, false), kk > 0);
   }
+}
+
+// The same with A's rows (bf16 pairs) in TMEM.
+template <int D>
+__device__ __forceinline__ void mma_scores_ta(int lead, uint32_t tmem_d, uint32_t tmem_a, uint32_t b) {
+  const uint64_t db = smem_desc(b, 16, 1024);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    mma_ts(lead, tmem_d, tmem_a + kk * 8, db + (((kk >> 2) * kBoxBytes + (kk & 3) * 32) >> 4), idesc(kTile, false),
+           kk > 0);
 }
 
 // D (TMEM, 128 x D) += A B: A 128 x 128 bf16 pairs in TMEM, 32 columns of it at
@@ -258,6 +272,45 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
   const bool bidir = p.b.bidir != 0;
+  bool ok = true;
+  // After a timed-out wait a thread stops waiting but keeps arriving, so
+  // the MMA thread is not left waiting on it; its rows are written as NaN.
+  auto wait = [&](int slot, int phase) {
+    if (ok && !wait_phase(c.bar0 + 8u * slot, phase, c.abort)) ok = false;
+  };
+  // A warp's arrival, once all of its lanes are there: an arrival per lane
+  // costs an operation on the barrier's word each.
+  auto arrive = [&](int slot) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(c.bar0 + 8u * slot);
+  };
+  if (DQ) {
+    // The rows of Q (groups 0, 1) and dO (2, 3) from their staged tiles into
+    // TMEM, as A operands: bf16 pairs as they lie in memory.
+    constexpr int kWords = D / 4;
+    const int row = quarter * 32 + lane;
+    const uint8_t* tile = c.smem + C::kSmRes + (g >> 1) * C::kTileBytes;
+    const uint32_t dst = c.tmem + ((uint32_t)(quarter * 32) << 16) + kColA + (g >> 1) * (D / 2) + (g & 1) * kWords;
+    wait(kBarRes, 0);
+#pragma unroll
+    for (int k = 0; k < kWords; k += 16) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int chunk = ((g & 1) * kWords + k) / 4 + i;  // 16 bytes of the row, 8 to a box row
+        const float4 u = *reinterpret_cast<const float4*>(tile + (chunk >> 3) * kBoxBytes + row * 128 +
+                                                          (((chunk & 7) ^ (row & 7)) << 4));
+        v[4 * i] = u.x;
+        v[4 * i + 1] = u.y;
+        v[4 * i + 2] = u.z;
+        v[4 * i + 3] = u.w;
+      }
+      tmem_st16(dst + k, v);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    arrive(kBarRes + 1);
+  }
   // The row statistics come from the kernel before this one; Q, K, V and dO
   // are older than that kernel's start.
   dependency_wait();
@@ -271,49 +324,37 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
       ndelta[i] = st.y;
     }
   }
-  bool ok = true;
-  // After a timed-out wait a thread stops waiting but keeps arriving, so
-  // the MMA thread is not left waiting on it; its rows are written as NaN.
-  auto wait = [&](int slot, int phase) {
-    if (ok && !wait_phase(c.bar0 + 8u * slot, phase, c.abort)) ok = false;
-  };
-  // A warp's arrival, once all of its lanes are there: an arrival per lane
-  // costs an operation on the barrier's word each.
-  auto arrive = [&](int slot) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar0 + 8u * slot);
-  };
+  // Tiles [full0, full1) of the sequence have every pair visible.
+  int full0, full1;
+  if (DQ) {  // reference keys alone, none after the first query unless all prefix rows see them
+    const int q0 = w.tile * kTile;
+    full0 = 0;
+    full1 = (bidir || q0 >= w.ref ? w.ref : min(w.ref, q0 + 1)) / kTile;
+  } else {   // no query before the last key, past the document, or past the first key's window
+    const int k0 = w.tile * kTile, first = c.seq.at(0) * kTile;
+    const bool all_ref = k0 + kTile <= w.ref;
+    const int from = all_ref && bidir ? 0 : k0 + kTile - 1;
+    const long long to = all_ref ? w.len : min((long long)w.len, (long long)k0 + p.b.n);
+    full0 = max(0, from - first + kTile - 1) / kTile;
+    full1 = (int)((to - first) / kTile);
+  }
   for (int j = w.lo; j < w.hi; ++j) {
     const int it = j - w.lo;
     const int o0 = c.seq.at(j) * kTile;  // first local row of the streamed tile
-    const uint32_t tS = base + (DQ ? (it & 1) * 256 : (it & 1) * 128);
+    const uint32_t tS = base + (DQ ? 0 : (it & 1) * 128);
     const uint32_t tP = base + (DQ ? 128 : ((it & 1) ^ 1) * 128);
-    // whether every pair of the tiles is visible; otherwise the visible columns
-    // of the thread's rows
-    bool full;
-    uint32_t vis[4];
-    if (DQ) {
-      const int q0 = w.tile * kTile;
-      full = o0 + kTile <= w.ref && (bidir || q0 >= w.ref || o0 + kTile - 1 <= q0);
-      if (!full) {
+    const bool full = j >= full0 && j < full1;
+    uint32_t vis[4];  // otherwise: the visible columns of the thread's rows
+    if (!full) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int own = own0 + 8 * i, x0 = o0 + c0;
+      for (int i = 0; i < 4; ++i) {
+        const int own = own0 + 8 * i, x0 = o0 + c0;
+        if (DQ)
           vis[i] = own < w.ref ? bit_range(0, (bidir ? w.ref : own + 1) - x0)
                                : bit_range(0, w.ref - x0) | bit_range(max(w.ref, own - p.b.n + 1) - x0, own + 1 - x0);
-        }
-      }
-    } else {
-      const int k0 = w.tile * kTile, last = o0 + kTile - 1;
-      full = last < w.len && ((k0 + kTile <= w.ref && (bidir || k0 + kTile - 1 <= o0)) ||
-                              (k0 + kTile - 1 <= o0 && (long long)k0 + p.b.n > last));
-      if (!full) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int own = own0 + 8 * i, x0 = o0 + c0;
+        else
           vis[i] = bit_range((own < w.ref && bidir ? 0 : own) - x0,
                              (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - x0);
-        }
       }
     }
     const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it & 1) * 2 * kTile + c0;
@@ -323,6 +364,10 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     float x[kCols];
     tmem_ld_frag(tS, x);
     tmem_wait_ld();
+    if (DQ) {
+      tc_fence_before();
+      arrive(kBarRead);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float2 l = make_float2(0.f, 0.f);
@@ -361,8 +406,10 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     float dp[kCols];
     tmem_ld_frag(tP, dp);
     tmem_wait_ld();
-    tc_fence_before();
-    arrive(kBarDPRead);
+    if (!DQ) {
+      tc_fence_before();
+      arrive(kBarRead);
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float2 d = make_float2(0.f, 0.f);
@@ -375,7 +422,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     }
     // a masked weight of 0 times a NaN of another document's row
     if (!full) keep(x, vis, ft);
-    tmem_st_frag(DQ ? tS : tS + kCols / 2, x);
+    tmem_st_frag(DQ ? tP : tS + kCols / 2, x);
     tmem_wait_st();
     tc_fence_before();
     arrive(kBarDS + (it & 1));
@@ -441,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(B(kBarRes + s), 1);
+      mbar_init(B(kBarRes + s), dq && s == 1 ? kSoftmaxThreads / 32 : 1);
       mbar_init(B(kBarS + s), 1);
       mbar_init(B(kBarStats + s), 1);
       mbar_init(B(kBarP + s), kSoftmaxThreads / 32);
@@ -454,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(B(kBarBFree + s), 1);
     }
     mbar_init(B(kBarDP), 1);
-    mbar_init(B(kBarDPRead), kSoftmaxThreads / 32);
+    mbar_init(B(kBarRead), kSoftmaxThreads / 32);
     mbar_init(B(kBarFinal), 1);
     *s_abort = (sbase & 1023) != 0;
     fence_barrier_init();
@@ -482,7 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
       const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
-      load(smRes, dq ? &p.tmQ : &p.tmK, w.tile, B(kBarRes));
+      if (dq) {
+        mbar_arrive_expect_tx(B(kBarRes), 2 * C::kTileBytes);
+        for (int x = 0; x < C::kBoxes; ++x) {
+          tma_load_3d(smRes + x * kBoxBytes, &p.tmQ, kBox * x, h, w.start + w.tile * kTile, B(kBarRes));
+          tma_load_3d(smRes + C::kTileBytes + x * kBoxBytes, &p.tmG, kBox * x, h, w.start + w.tile * kTile, B(kBarRes));
+        }
+      } else {
+        load(smRes, &p.tmK, w.tile, B(kBarRes));
+      }
       int a = 0, b = 0;  // tiles issued on each ring
       bool ok = true;
       for (int j = 0; j < nt && ok; ++j) {
@@ -491,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         load(smA + (j % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + j % nA));
         ++a;
-        if (j == 0) load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, w.tile, B(kBarRes + 1));
+        if (j == 0 && !dq) load(smRes + C::kTileBytes, &p.tmV, w.tile, B(kBarRes + 1));
         ok = !*s_abort && mbar_wait_bounded(B(kBarBFree + j % nB), ((j / nB) & 1) ^ 1);
         if (!ok) break;
         load(smB + (j % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + j % nB));
@@ -500,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) *s_abort = 1;
       // drain: every issued copy has landed before the CTA may exit
       mbar_wait_bounded(B(kBarRes), 0);
-      if (a > 0) mbar_wait_bounded(B(kBarRes + 1), 0);
+      if (!dq && a > 0) mbar_wait_bounded(B(kBarRes + 1), 0);
       for (int j = max(0, a - nA); j < a; ++j) mbar_wait_bounded(B(kBarAFull + j % nA), (j / nA) & 1);
       for (int j = max(0, b - nB); j < b; ++j) mbar_wait_bounded(B(kBarBFull + j % nB), (j / nB) & 1);
     }
@@ -516,31 +571,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto tileB = [&](int j) { return smB + (j % nB) * C::kTileBytes; };
       bool ok;
       if (dq) {
-        const uint32_t dP = tmem + 128, dQ = tmem + 384;
+        const uint32_t S = tmem, dP = tmem + 128, dQ = tmem + 384, aQ = tmem + kColA, aG = aQ + D / 2;
         auto scores = [&](int j) -> bool {  // S(j) = Q K_j^T
           if (!wait(kBarAFull + j % nA, j / nA)) return false;
           tc_fence_after();
-          mma_scores<D>(lead, tmem + (j & 1) * 256, smRes, tileA(j));
+          mma_scores_ta<D>(lead, S, aQ, tileA(j));
           commit(lead, B(kBarS + (j & 1)));
           return true;
         };
         auto dprob = [&](int j) -> bool {  // dP(j) = dO V_j^T
           if (!wait(kBarBFull + j % nB, j / nB)) return false;
           tc_fence_after();
-          mma_scores<D>(lead, dP, smRes + C::kTileBytes, tileB(j));
+          mma_scores_ta<D>(lead, dP, aG, tileB(j));
           commit(lead, B(kBarDP));
           commit(lead, B(kBarBFree + j % nB));
           return true;
         };
-        ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0) && (nt < 2 || scores(1));
+        ok = wait(kBarRes + 1, 0) && scores(0) && dprob(0);
         for (int j = 0; j < nt && ok; ++j) {
-          if (j + 1 < nt) ok = wait(kBarDPRead, j) && dprob(j + 1);
+          if (j + 1 < nt) ok = wait(kBarRead, j) && scores(j + 1);
           ok = ok && wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(lead, dQ, tmem + (j & 1) * 256, tileA(j), j > 0);
+          mma_grad<D>(lead, dQ, dP, tileA(j), j > 0);
           commit(lead, B(kBarAFree + j % nA));
-          if (j + 2 < nt) ok = scores(j + 2);
+          if (j + 1 < nt) ok = dprob(j + 1);
         }
       } else {
         const uint32_t dV = tmem + 256, dK = tmem + 384;
@@ -565,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           mma_grad<D>(lead, dV, tmem + (j & 1) * 128, tileB(j), j > 0);
           commit(lead, B(kBarBFree + j % nB));
-          if (j + 1 < nt) ok = wait(kBarDPRead, j) && scores(j + 1);
+          if (j + 1 < nt) ok = wait(kBarRead, j) && scores(j + 1);
           ok = ok && wait(kBarDS + (j & 1), j >> 1);
           if (!ok) break;
           tc_fence_after();
