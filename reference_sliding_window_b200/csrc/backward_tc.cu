@@ -235,9 +235,22 @@ __device__ __forceinline__ void keep(float* x, const uint32_t* vis, int t) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float& y = x[16 * (i >> 1) + 2 * (i & 1) + 4 * (e >> 1) + (e & 1)];
-      y = __uint_as_float(__float_as_uint(y) & (uint32_t)((int)(bits << (31 - 8 * (e >> 1) - (e & 1))) >> 31));
+      y = bits & (1u << (8 * (e >> 1) + (e & 1))) ? y : 0.f;
     }
   }
+}
+
+// Transposes the 4 x 4 words of a quad of lanes: q[j] of lane t becomes q[t] of lane j.
+__device__ __forceinline__ void quad_transpose(uint32_t* q, int t) {
+#pragma unroll
+  for (int b = 1; b <= 2; b <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(i & b)) {
+        const uint32_t x = __shfl_xor_sync(0xffffffffu, t & b ? q[i] : q[i | b], b);
+        if (t & b) q[i] = x;
+        else q[i | b] = x;
+      }
 }
 
 // A bounded wait that ends early once the CTA has given up.
@@ -380,20 +393,18 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
         y[1] = ex2(y[1]);
       }
     }
-    if (!full) {
-      keep(x, vis, ft);
-      // rows of the streamed tiles past the document's end
+    const bool past_end = o0 + kTile > w.len;
+    if (!full) keep(x, vis, ft);
+    if (past_end) {  // rows of the streamed tiles past the document's end
       const int valid = w.len - o0;
-      if (valid < kTile) {
-        for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
-          const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
-          const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(c.smem + C::kSmA + (it % nA) * C::kTileBytes + off) = zero;
-          if (!DQ) *reinterpret_cast<uint4*>(c.smem + C::kSmB + (it % nB) * C::kTileBytes + off) = zero;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
+        const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
+        const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(c.smem + C::kSmA + (it % nA) * C::kTileBytes + off) = zero;
+        if (!DQ) *reinterpret_cast<uint4*>(c.smem + C::kSmB + (it % nB) * C::kTileBytes + off) = zero;
       }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (!DQ) {
       tmem_st_frag(tS, x);
@@ -421,7 +432,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
       }
     }
     // a masked weight of 0 times a NaN of another document's row
-    if (!full) keep(x, vis, ft);
+    if (past_end) keep(x, vis, ft);
     tmem_st_frag(DQ ? tP : tS + kCols / 2, x);
     tmem_wait_st();
     tc_fence_before();
@@ -432,33 +443,42 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   tc_fence_after();
   if (!ok) *c.abort = 1;
   const bool good = ok && !*c.abort;
-  // dQ: each group a quarter of the columns; dK, dV: groups 0, 1 halves of dV, 2, 3 of dK
-  constexpr int kMine = DQ ? D / 4 : D / 2;
-  const int r = quarter * 32 + lane, own = w.tile * kTile + r;  // one row per thread here
-  const int col0 = (DQ ? g : g & 1) * kMine, which = DQ ? 0 : g >> 1;
-  const uint32_t src = c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col0;
+  // Blocks of 32 columns, a group each in turn: those of dQ, or of dV, then dK.
+  constexpr int kBlocks = D / 32;
   const int H = p.b.H;
-  float* part = w.part < 0 ? nullptr
-                           : p.b.partials + (((size_t)w.part * H + c.h) * 2 + which) * kTile * D + r * D + col0;
-  __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
-                        ((size_t)(w.start + own) * H + c.h) * D + col0;
-  const float mul = !good ? __int_as_float(0x7fc00000) : part || (!DQ && which == 0) ? 1.f : p.b.scale;
 #pragma unroll 1
-  for (int k = 0; k < kMine; k += 16) {
-    float o[16];
-    tmem_ld16(src + k, o);
+  for (int blk = g; blk < (DQ ? 1 : 2) * kBlocks; blk += 4) {
+    const int which = blk / kBlocks, col = blk % kBlocks * 32;
+    float o[32];
+    tmem_ld_frag(c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col, o);
     tmem_wait_ld();
-    if (own < w.len) {
+    if (w.part < 0) {
+      const float mul = !good ? __int_as_float(0x7fc00000) : !DQ && which == 0 ? 1.f : p.b.scale;
+      __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
+                            ((size_t)(w.start + own0) * H + c.h) * D + col + 8 * ft;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) o[e] *= mul;
-      if (part) {
+      for (int i = 0; i < 4; ++i) {
+        const float* v = o + 16 * (i >> 1) + 2 * (i & 1);
+        uint32_t q[4];
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          *reinterpret_cast<float4*>(part + k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; e += 8) *reinterpret_cast<uint4*>(grad + k + e) = pack16<__nv_bfloat16>(o + e);
+        for (int k = 0; k < 4; ++k) q[k] = pack_bf16x2(v[4 * k] * mul, v[4 * k + 1] * mul);
+        // Words to the lane that holds their 16 bytes: a warp then writes 64
+        // bytes of 8 rows at a time (a row per lane costs a pass per line).
+        quad_transpose(q, ft);
+        if (own0 + 8 * i < w.len)
+          *reinterpret_cast<uint4*>(grad + (size_t)(8 * i) * H * D) = make_uint4(q[0], q[1], q[2], q[3]);
       }
+    } else {
+      float* part = p.b.partials + (((size_t)w.part * H + c.h) * 2 + which) * kTile * D +
+                    (quarter * 32 + fg) * D + col + 2 * ft;
+      const float mul = good ? 1.f : __int_as_float(0x7fc00000);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float* v = o + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+          *reinterpret_cast<float2*>(part + 8 * i * D + 8 * k) = make_float2(v[0] * mul, v[1] * mul);
+        }
     }
   }
 }
