@@ -68,6 +68,9 @@ Plan make_plan(int size, const int32_t* cu, const int32_t* refs, int n_docs, int
 int tile_size(int elem) { return elem == kBF16 ? kBwdTileTc : kBwdTileF32; }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+// Launches of a plan's items (never more than the threads that form the statistics).
+int n_launches(const Plan& plan) { return (int)((plan.work.size() + kBwdMaxWork - 1) / kBwdMaxWork); }
+size_t counter_bytes(const Plan& plan) { return align_up(sizeof(int32_t) * (size_t)n_launches(plan)); }
 size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * (L + 128)); }
 
 // Row statistics, float32: D/N lanes per row
@@ -77,6 +80,7 @@ __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParam
   constexpr int N = Vec16<T>::N, G = D / N;
   launch_dependents();  // the items load their tiles while the statistics form
   const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (idx < p.n_counters) p.counter[idx] = 0;
   const long long rh = idx / G;  // row * H + head
   const int e = (int)(idx % G) * N;
   const bool in = rh < (long long)p.L * p.H;
@@ -149,15 +153,18 @@ size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_do
                                 bool bidir) {
   const int size = tile_size(elem);
   const Plan plan = make_plan(size, cu, refs, n_docs, n, H, bidir);
-  return stats_bytes(cu[n_docs], H) + sizeof(float) * (size_t)plan.parts * H * 2 * size * D;
+  return counter_bytes(plan) + stats_bytes(cu[n_docs], H) + sizeof(float) * (size_t)plan.parts * H * 2 * size * D;
 }
 
 cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStream_t stream) {
   const int size = tile_size(elem);
   const Plan plan = make_plan(size, p.cu, p.refs, p.n_docs, p.n, p.H, p.bidir != 0);
-  p.stats = static_cast<float2*>(workspace);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.counter = reinterpret_cast<int32_t*>(ws);
+  p.n_counters = n_launches(plan);
+  p.stats = reinterpret_cast<float2*>(ws + counter_bytes(plan));
   p.stat_stride = p.L + 128;
-  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + stats_bytes(p.L, p.H));
+  p.partials = reinterpret_cast<float*>(ws + counter_bytes(plan) + stats_bytes(p.L, p.H));
   cudaError_t e = elem == kF32 ? (p.D == 64 ? launch_stats<float, 64>(p, stream) : launch_stats<float, 128>(p, stream))
                   : p.D == 64  ? launch_stats<__nv_bfloat16, 64>(p, stream)
                                : launch_stats<__nv_bfloat16, 128>(p, stream);

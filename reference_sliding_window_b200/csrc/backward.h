@@ -88,6 +88,8 @@ struct BackwardParams {
   float2* stats;    // [H][stat_stride]: (-lse log2 e, -delta) of each row
   int stat_stride;  // at least L + 128: a tile's rows may reach past the pack
   float* partials;  // [parts][H][2][tile][D]
+  int32_t* counter; // one per launch: items taken off its list, zeroed with the statistics
+  int n_counters;
 };
 
 constexpr int kBwdTileTc = 128, kBwdTileF32 = 64;

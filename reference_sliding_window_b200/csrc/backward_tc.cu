@@ -2,7 +2,8 @@
 // cores (tcgen05 + TMEM): bf16 tensors, head dim 64 or 128, float32
 // accumulation.  The formulas, the mask and the work items are in backward.h.
 //
-// One CTA per work item and head, tiles of 128 queries x 128 keys.  Bound: the
+// One CTA per SM, which takes (work item, head) pairs off a counter, heaviest
+// first; tiles of 128 queries x 128 keys.  Bound: the
 // tensor pipe (4 tile products per key tile and query tile in a dK, dV item, 3
 // in a dQ item), with the exponentials and the products' operand reads from
 // shared memory close behind.
@@ -19,7 +20,7 @@
 //   writes); with A in TMEM it takes 68.  A dK, dV item has no TMEM left for it.
 // * Warp 0 streams tiles with TMA (128-byte swizzle) through two rings, warp
 //   1 issues the MMAs, warp 2 stages the row statistics (dK, dV items, where
-//   they vary along a thread's columns), warps 4-19 are the softmax: four
+//   they vary along a thread's columns), warps 3-18 are the softmax: four
 //   groups of 128 threads, one thread per TMEM lane and a quarter of its 128
 //   columns.
 // * Issue order of a dK, dV item, two score regions X, Y taking turns: S(i)
@@ -34,7 +35,13 @@
 // * Rows of a streamed tile past the document's end belong to the next
 //   document.  Their weights are exactly 0, but 0 times an infinity is NaN, so
 //   the softmax clears them in shared memory before the products read them.
-// * Every wait is bounded; on a timeout the item's rows are written as NaN.
+// * The producer takes the next item while the last tiles of the current one are
+//   computed and starts its loads (a load under way from memory takes 2 to 3
+//   us, as long as a short document's whole item): every role walks the items
+//   by itself, and barriers, not the CTA's start, order one item's use of a tile,
+//   a region or an accumulator before the next one's.
+// * Every wait is bounded; on a timeout the rows of the CTA's items are written
+//   as NaN.
 
 #include <algorithm>
 
@@ -46,10 +53,11 @@ namespace rswa {
 namespace tc {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kSoftmaxWarp = 4;
+constexpr int kThreads = 608;
+constexpr int kSoftmaxWarp = 3;
 constexpr int kSoftmaxThreads = 512;
-constexpr int kCols = 32;  // score columns of a softmax thread
+constexpr int kCols = 32;                          // score columns of a fragment block
+constexpr int kPer = 4 * 128 / kSoftmaxThreads;    // blocks of a softmax thread
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColA = 256;  // dQ items: the rows of Q, then of dO, bf16 pairs
 
@@ -57,6 +65,7 @@ struct BwdTcParams {
   CUtensorMap tmQ, tmK, tmV, tmG;  // packed [L][H][D] maps; G is dO
   BackwardParams b;
   float scale_log2;
+  int n_items;  // work entries x heads
 };
 
 template <int D>
@@ -80,23 +89,29 @@ static_assert(Cfg<128>::kSmBytes <= 232448 && Cfg<64>::kSmBytes <= 232448, "shar
 
 // A wait names one of a barrier's two phases, so a barrier's next phase but one
 // must not complete while a waiter has still to see this one.  S, P and dS take
-// two barriers in turn; everything else is ordered by the ring's or the region's
-// next use.  (Warp 2's wait for dS(j) comes before it stages the statistics that
-// dS(j+2) needs.)
+// two barriers in turn; everything else is ordered by the next use of the ring,
+// region, tile or slot that it guards.  Phases count over all items of the CTA.
 enum : int {
-  kBarRes = 0,      // 2: the item's own tiles; dQ items: both have landed, both are in TMEM
-  kBarAFull = 2,    // 4
-  kBarAFree = 6,    // 4
-  kBarBFull = 10,   // 4
-  kBarBFree = 14,   // 4
-  kBarS = 18,       // 2
-  kBarP = 20,       // 2
-  kBarDS = 22,      // 2
-  kBarDP = 24,
-  kBarRead = 25,    // dK, dV items: dP is read; dQ items: S is
-  kBarFinal = 26,
-  kBarStats = 27,   // 2
-  kSlotTmem = 29, kSlotAbort = 30
+  kBarRes = 0,        // 2: the item's own tiles have landed (K, V or Q, dO)
+  kBarResFree = 2,    // they may be overwritten
+  kBarRows = 3,       // dQ items: Q and dO are in TMEM
+  kBarAccFree = 4,    // the item's accumulators have been read
+  kBarItem = 5,       // 2: the next item's number is in its slot
+  kBarItemFree = 7,   // 2: every role is done with the item
+  kBarAFull = 9,      // 4
+  kBarAFree = 13,     // 4
+  kBarBFull = 17,     // 4
+  kBarBFree = 21,     // 4
+  kBarS = 25,         // 2
+  kBarP = 27,         // 2 (dK, dV items)
+  kBarDS = 29,        // 2
+  kBarDP = 31,
+  kBarRead = 32,      // dK, dV items: dP is read; dQ items: S is
+  kBarFinal = 33,     // the item's last MMA is done
+  kBarStats = 34,     // 2 (dK, dV items)
+  kBarStatsFree = 36, // 2
+  kBarEnd = 38,
+  kSlotTmem = 39, kSlotAbort = 40, kSlotItem = 42  // 2 x 32 bytes: {number, T, U, kq, len, ref}
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -226,17 +241,13 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
   const uint32_t below_lo = lo <= 0 ? 0u : lo >= 32 ? ~0u : (1u << lo) - 1;
   return below_hi & ~below_lo;
 }
-// Fragment elements zeroed (whatever they hold, NaN included) where the bit of
-// their column, vis[i] for row 8 i + g, is clear.
-__device__ __forceinline__ void keep(float* x, const uint32_t* vis, int t) {
+// A fragment's row i (of 4): its elements zeroed (whatever they hold, NaN
+// included) where the bit of their column is clear.
+__device__ __forceinline__ void keep_row(float* x, int i, uint32_t bits) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t bits = vis[i] >> (2 * t);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float& y = x[16 * (i >> 1) + 2 * (i & 1) + 4 * (e >> 1) + (e & 1)];
-      y = bits & (1u << (8 * (e >> 1) + (e & 1))) ? y : 0.f;
-    }
+  for (int e = 0; e < 8; ++e) {
+    float& y = x[16 * (i >> 1) + 2 * (i & 1) + 4 * (e >> 1) + (e & 1)];
+    y = bits & (1u << (8 * (e >> 1) + (e & 1))) ? y : 0.f;
   }
 }
 
@@ -253,76 +264,138 @@ __device__ __forceinline__ void quad_transpose(uint32_t* q, int t) {
       }
 }
 
-// A bounded wait that ends early once the CTA has given up.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, int phase, volatile int* abort) {
-  return mbar_try_wait(bar, phase & 1) || (!*abort && mbar_wait_bounded(bar, phase & 1));
+__device__ __forceinline__ int ld_shared(uint32_t addr) {
+  int v;
+  asm volatile("ld.volatile.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, int v) {
+  asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float2 ld_shared2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
 }
 
-struct Ctx {
-  const BwdTcParams& p;
-  const BwdWork& w;
-  const BwdTiles& seq;
-  uint8_t* smem;
-  uint32_t bar0, tmem;
-  volatile int* abort;
-  int h;
+// A bounded wait (bar0: the barriers' base) that ends early once the CTA has given up.
+__device__ __forceinline__ bool wait_phase(uint32_t bar0, int slot, int phase) {
+  const uint32_t bar = bar0 + 8u * slot;
+  return mbar_try_wait(bar, phase & 1) || (!ld_shared(bar0 + 8u * kSlotAbort) && mbar_wait_bounded(bar, phase & 1));
+}
+
+// The item that a role works on.  What the CTA did before it comes from the
+// item's slot, so that no role carries it in registers from item to item.
+struct Item {
+  BwdWork w;
+  BwdTiles seq;
+  int h, nt;
+  bool dq;
+  int T;      // tiles before it
+  int U;      // of them dK, dV items' tiles
+  int kq;     // dQ items before it
+  int k = 0;  // items before it
+
+  // The next item, read by all lanes of a warp; false: there is none.
+  template <typename P>
+  __device__ __forceinline__ bool next(uint32_t bar0, const P& p) {
+    return announced(bar0, k) && read(bar0, p);
+  }
+  template <typename P>
+  __device__ __forceinline__ bool read(uint32_t bar0, const P& p) {
+    const uint32_t s = slot(bar0, k);
+    const int id = k == 0 ? (int)blockIdx.x : ld_shared(s);
+    if (id < 0) return false;
+    T = k == 0 ? 0 : ld_shared(s + 4);
+    U = k == 0 ? 0 : ld_shared(s + 8);
+    kq = k == 0 ? 0 : ld_shared(s + 12);
+    decode(p, id);
+    return true;
+  }
+  static __device__ __forceinline__ uint32_t slot(uint32_t bar0, int k) { return bar0 + 8u * kSlotItem + 32u * (k & 1); }
+  // Whether item k has been announced (by all lanes of a warp).  Every role knows the first.
+  static __device__ __forceinline__ bool announced(uint32_t bar0, int k) {
+    return k == 0 || __all_sync(0xffffffffu, wait_phase(bar0, kBarItem + (k & 1), k >> 1));
+  }
+  template <typename P>
+  __device__ __forceinline__ void decode(const P& p, int id) {
+    w = p.work[id / p.b.H];
+    h = id % p.b.H;
+    dq = w.kind == kBwdDQ;
+    seq = dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0)
+             : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0);
+    nt = w.hi - w.lo;
+  }
+  // Gives the slot back (one arrival per warp).
+  __device__ __forceinline__ void done(uint32_t bar0, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar0 + 8u * (kBarItemFree + (k & 1)));
+    ++k;
+  }
 };
 
 // The softmax warps of an item: P and dS of every tile of its sequence, then
 // the finished gradient tile from TMEM to memory.
-template <int D, bool DQ>
-__device__ __forceinline__ void softmax_warps(const Ctx& c) {
+template <int D, bool DQ, typename P>
+__device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const P& p, int item_k, bool& ok) {
   using C = Cfg<D>;
   constexpr int nA = C::kA, nB = C::kB;
-  const BwdTcParams& p = c.p;
-  const BwdWork& w = c.w;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Item item;
+  item.k = item_k;
+  item.read(bar0, p);
+  const BwdWork& w = item.w;
+  const BwdTiles& seq = item.seq;
+  // Opaque, so that what follows from it is worked out per item, not kept in
+  // registers over all of them for both kinds.
+  int tid = threadIdx.x;
+  asm volatile("" : "+r"(tid), "+r"(bar0), "+r"(tmem));
+  const int warp = tid >> 5, lane = tid & 31;
   const int g = (warp - kSoftmaxWarp) >> 2;  // column quarter
   const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
   const int fg = lane >> 2, ft = lane & 3;   // the fragments' row and column pair
-  const int c0 = kCols * g;
+  const int c0 = kPer * kCols * g;
   const int own0 = w.tile * kTile + quarter * 32 + fg;  // the thread's local rows own0 + 8 i: queries (DQ) or keys
-  const uint32_t base = c.tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+  const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
   const bool bidir = p.b.bidir != 0;
-  bool ok = true;
   // After a timed-out wait a thread stops waiting but keeps arriving, so
   // the MMA thread is not left waiting on it; its rows are written as NaN.
   auto wait = [&](int slot, int phase) {
-    if (ok && !wait_phase(c.bar0 + 8u * slot, phase, c.abort)) ok = false;
+    if (ok && !wait_phase(bar0, slot, phase)) ok = false;
   };
   // A warp's arrival, once all of its lanes are there: an arrival per lane
   // costs an operation on the barrier's word each.
   auto arrive = [&](int slot) {
     __syncwarp();
-    if (lane == 0) mbar_arrive(c.bar0 + 8u * slot);
+    if (lane == 0) mbar_arrive(bar0 + 8u * slot);
   };
   if (DQ) {
-    // The rows of Q (groups 0, 1) and dO (2, 3) from their staged tiles into
-    // TMEM, as A operands: bf16 pairs as they lie in memory.
-    constexpr int kWords = D / 4;
-    const int row = quarter * 32 + lane;
-    const uint8_t* tile = c.smem + C::kSmRes + (g >> 1) * C::kTileBytes;
-    const uint32_t dst = c.tmem + ((uint32_t)(quarter * 32) << 16) + kColA + (g >> 1) * (D / 2) + (g & 1) * kWords;
-    wait(kBarRes, 0);
+    // The rows of Q and dO from their staged tiles into TMEM, as A operands: bf16
+    // pairs as they lie in memory; a group takes an equal share of the words.
+    constexpr int kWords = D * 128 / kSoftmaxThreads;  // of the D words of both rows
+    const int row = quarter * 32 + lane, word0 = g * kWords, which = word0 / (D / 2);
+    const uint32_t tile = bar0 - C::kSmBar + C::kSmRes + which * C::kTileBytes;
+    const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kColA + word0;
+    if (item.k > 0) wait(kBarAccFree, item.k - 1);  // (over the last item's dV)
+    wait(kBarRes + which, item.k);
+    tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kWords; k += 16) {
       float v[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int chunk = ((g & 1) * kWords + k) / 4 + i;  // 16 bytes of the row, 8 to a box row
-        const float4 u = *reinterpret_cast<const float4*>(tile + (chunk >> 3) * kBoxBytes + row * 128 +
-                                                          (((chunk & 7) ^ (row & 7)) << 4));
-        v[4 * i] = u.x;
-        v[4 * i + 1] = u.y;
-        v[4 * i + 2] = u.z;
-        v[4 * i + 3] = u.w;
+        const int chunk = (word0 % (D / 2) + k) / 4 + i;  // 16 bytes of the row, 8 to a box row
+        const uint32_t u = tile + (chunk >> 3) * kBoxBytes + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[4 * i]), "=f"(v[4 * i + 1]), "=f"(v[4 * i + 2]), "=f"(v[4 * i + 3])
+                     : "r"(u)
+                     : "memory");
       }
       tmem_st16(dst + k, v);
     }
     tmem_wait_st();
     tc_fence_before();
-    arrive(kBarRes + 1);
+    arrive(kBarRows);
   }
   // The row statistics come from the kernel before this one; Q, K, V and dO
   // are older than that kernel's start.
@@ -331,7 +404,7 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
   if (DQ) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)c.h * p.b.stat_stride + w.start + own0 + 8 * i]
+      const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)item.h * p.b.stat_stride + w.start + own0 + 8 * i]
                                              : make_float2(0.f, 0.f);
       nlse[i] = st.x;
       ndelta[i] = st.y;
@@ -344,118 +417,150 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
     full0 = 0;
     full1 = (bidir || q0 >= w.ref ? w.ref : min(w.ref, q0 + 1)) / kTile;
   } else {   // no query before the last key, past the document, or past the first key's window
-    const int k0 = w.tile * kTile, first = c.seq.at(0) * kTile;
+    const int k0 = w.tile * kTile, first = seq.at(0) * kTile;
     const bool all_ref = k0 + kTile <= w.ref;
     const int from = all_ref && bidir ? 0 : k0 + kTile - 1;
     const long long to = all_ref ? w.len : min((long long)w.len, (long long)k0 + p.b.n);
     full0 = max(0, from - first + kTile - 1) / kTile;
     full1 = (int)((to - first) / kTile);
   }
-  for (int j = w.lo; j < w.hi; ++j) {
-    const int it = j - w.lo;
-    const int o0 = c.seq.at(j) * kTile;  // first local row of the streamed tile
-    const uint32_t tS = base + (DQ ? 0 : (it & 1) * 128);
-    const uint32_t tP = base + (DQ ? 128 : ((it & 1) ^ 1) * 128);
-    const bool full = j >= full0 && j < full1;
-    uint32_t vis[4];  // otherwise: the visible columns of the thread's rows
-    if (!full) {
+  // (what only a masked tile needs is read back from the item's slot)
+  const int nt = item.nt, T = item.T, U = item.U, f0 = full0 - w.lo, f1 = full1 - w.lo;
+  const BwdTiles tiles = {seq.A - w.lo, seq.B0 + (DQ ? 0 : w.lo), w.lo};
+#pragma unroll 1
+  for (int j = 0; j < nt; ++j) {
+    const int odd = j & 1, it = T + j, iu = U + j;
+    // first local row of the streamed tile
+    const int o0 = (DQ ? (j < tiles.A ? j + tiles.nB : tiles.B0 + j - tiles.A) : tiles.B0 + j) * kTile;
+    const uint32_t tS = base + (DQ ? 0 : odd * 128);
+    const uint32_t tP = base + (DQ ? 128 : (odd ^ 1) * 128);
+    const bool full = j >= f0 && j < f1;
+    const uint32_t slot = Item::slot(bar0, item_k);
+    // Zeroes what the thread's rows do not see of block q.
+    auto mask = [&](float* y, int q, int len, int ref) {
+      const int x0 = o0 + c0 + kCols * q, n = min(p.b.n, len);  // (own + n stays small)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int own = own0 + 8 * i, x0 = o0 + c0;
+        const int own = own0 + 8 * i;
+        uint32_t vis;
         if (DQ)
-          vis[i] = own < w.ref ? bit_range(0, (bidir ? w.ref : own + 1) - x0)
-                               : bit_range(0, w.ref - x0) | bit_range(max(w.ref, own - p.b.n + 1) - x0, own + 1 - x0);
+          vis = own < ref ? bit_range(0, (bidir ? ref : own + 1) - x0)
+                          : bit_range(0, ref - x0) | bit_range(max(ref, own - n + 1) - x0, own + 1 - x0);
         else
-          vis[i] = bit_range((own < w.ref && bidir ? 0 : own) - x0,
-                             (own < w.ref ? w.len : (int)min((long long)w.len, (long long)own + p.b.n)) - x0);
+          vis = bit_range((own < ref && bidir ? 0 : own) - x0, (own < ref ? len : min(len, own + n)) - x0);
+        keep_row(y, i, vis >> (2 * ft));
       }
-    }
-    const float* st = reinterpret_cast<const float*>(c.smem + C::kSmStats) + (it & 1) * 2 * kTile + c0;
-    if (!DQ) wait(kBarStats + (it & 1), it >> 1);
+    };
+    const uint32_t st = bar0 - C::kSmBar + C::kSmStats + (iu & 1) * 1024 + (c0 + 2 * ft) * 4;
+    if (!DQ) wait(kBarStats + (iu & 1), iu >> 1);
     wait(kBarS + (it & 1), it >> 1);
     tc_fence_after();
-    float x[kCols];
-    tmem_ld_frag(tS, x);
+    float x[kPer * kCols];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) tmem_ld_frag(tS + kCols * q, x + kCols * q);
     tmem_wait_ld();
     if (DQ) {
       tc_fence_before();
       arrive(kBarRead);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4 * kPer; ++k) {
       float2 l = make_float2(0.f, 0.f);
-      if (!DQ) l = *reinterpret_cast<const float2*>(st + 8 * k + 2 * ft);
+      if (!DQ) l = ld_shared2(st + 32 * k);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float* y = x + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+        float* y = x + kCols * (k >> 2) + 16 * (i >> 1) + 2 * (i & 1) + 4 * (k & 3);
         fma2(y[0], y[1], sl2, DQ ? nlse[i] : l.x, DQ ? nlse[i] : l.y);
         y[0] = ex2(y[0]);
         y[1] = ex2(y[1]);
       }
     }
-    const bool past_end = o0 + kTile > w.len;
-    if (!full) keep(x, vis, ft);
-    if (past_end) {  // rows of the streamed tiles past the document's end
-      const int valid = w.len - o0;
-      for (int i = threadIdx.x - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
-        const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
-        const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(c.smem + C::kSmA + (it % nA) * C::kTileBytes + off) = zero;
-        if (!DQ) *reinterpret_cast<uint4*>(c.smem + C::kSmB + (it % nB) * C::kTileBytes + off) = zero;
+    bool past_end = false;
+    if (!full) {
+      const int len = ld_shared(slot + 16), ref = ld_shared(slot + 20);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) mask(x + kCols * q, q, len, ref);
+      past_end = o0 + kTile > len;
+      if (past_end) {  // rows of the streamed tiles past the document's end
+        const int valid = len - o0;
+        for (int i = tid - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
+          const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
+          const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
+          auto clear = [&](uint32_t stage) {
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(bar0 - C::kSmBar + stage + off), "r"(0)
+                         : "memory");
+          };
+          clear(C::kSmA + (it % nA) * C::kTileBytes);
+          if (!DQ) clear(C::kSmB + (it % nB) * C::kTileBytes);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (!DQ) {
-      tmem_st_frag(tS, x);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) tmem_st_frag(tS + kCols * q, x + kCols * q);
       tmem_wait_st();
       tc_fence_before();
-      arrive(kBarP + (it & 1));
+      arrive(kBarP + (iu & 1));
     }
     wait(kBarDP, it);
     tc_fence_after();
-    float dp[kCols];
-    tmem_ld_frag(tP, dp);
+    float dp[kPer * kCols];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) tmem_ld_frag(tP + kCols * q, dp + kCols * q);
     tmem_wait_ld();
     if (!DQ) {
       tc_fence_before();
       arrive(kBarRead);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float2 d = make_float2(0.f, 0.f);
-      if (!DQ) d = *reinterpret_cast<const float2*>(st + kTile + 8 * k + 2 * ft);
+    for (int q = 0; q < kPer; ++q) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
-        addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
+      for (int k = 0; k < 4; ++k) {
+        float2 d = make_float2(0.f, 0.f);
+        if (!DQ) d = ld_shared2(st + 4 * (kTile + kCols * q) + 32 * k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = kCols * q + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+          addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
+        }
       }
+      // a masked weight of 0 times a NaN of another document's row
+      if (past_end) mask(x + kCols * q, q, ld_shared(slot + 16), ld_shared(slot + 20));
+      tmem_st_frag((DQ ? tP : tS + kCols / 2) + kCols * q, x + kCols * q);
     }
-    // a masked weight of 0 times a NaN of another document's row
-    if (past_end) keep(x, vis, ft);
-    tmem_st_frag(DQ ? tP : tS + kCols / 2, x);
     tmem_wait_st();
     tc_fence_before();
-    arrive(kBarDS + (it & 1));
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bar0 + 8u * (kBarDS + (it & 1)));
+      if (!DQ) mbar_arrive(bar0 + 8u * (kBarStatsFree + (iu & 1)));
+    }
   }
   // -------------------------------------------------- the tile's gradient
-  wait(kBarFinal, 0);
+  wait(kBarFinal, item_k);
   tc_fence_after();
-  if (!ok) *c.abort = 1;
-  const bool good = ok && !*c.abort;
+  if (!ok) st_shared(bar0 + 8u * kSlotAbort, 1);
+  const bool good = ok && !ld_shared(bar0 + 8u * kSlotAbort);
+  // The item again from its slot: nothing of it but the loop's own stays in
+  // registers over the loop.
+  Item out;
+  out.k = item_k;
+  out.read(bar0, p);
+  const int own = out.w.tile * kTile + quarter * 32 + fg;
   // Blocks of 32 columns, a group each in turn: those of dQ, or of dV, then dK.
   constexpr int kBlocks = D / 32;
   const int H = p.b.H;
 #pragma unroll 1
-  for (int blk = g; blk < (DQ ? 1 : 2) * kBlocks; blk += 4) {
+  for (int blk = g; blk < (DQ ? 1 : 2) * kBlocks; blk += kSoftmaxThreads / 128) {
     const int which = blk / kBlocks, col = blk % kBlocks * 32;
     float o[32];
-    tmem_ld_frag(c.tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col, o);
+    tmem_ld_frag(tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col, o);
     tmem_wait_ld();
-    if (w.part < 0) {
+    if (out.w.part < 0) {
       const float mul = !good ? __int_as_float(0x7fc00000) : !DQ && which == 0 ? 1.f : p.b.scale;
       __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
-                            ((size_t)(w.start + own0) * H + c.h) * D + col + 8 * ft;
+                            ((size_t)(out.w.start + own) * H + out.h) * D + col + 8 * ft;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float* v = o + 16 * (i >> 1) + 2 * (i & 1);
@@ -465,11 +570,11 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
         // Words to the lane that holds their 16 bytes: a warp then writes 64
         // bytes of 8 rows at a time (a row per lane costs a pass per line).
         quad_transpose(q, ft);
-        if (own0 + 8 * i < w.len)
+        if (own + 8 * i < out.w.len)
           *reinterpret_cast<uint4*>(grad + (size_t)(8 * i) * H * D) = make_uint4(q[0], q[1], q[2], q[3]);
       }
     } else {
-      float* part = p.b.partials + (((size_t)w.part * H + c.h) * 2 + which) * kTile * D +
+      float* part = p.b.partials + (((size_t)out.w.part * H + out.h) * 2 + which) * kTile * D +
                     (quarter * 32 + fg) * D + col + 2 * ft;
       const float mul = good ? 1.f : __int_as_float(0x7fc00000);
 #pragma unroll
@@ -481,6 +586,8 @@ __device__ __forceinline__ void softmax_warps(const Ctx& c) {
         }
     }
   }
+  tc_fence_before();
+  arrive(kBarAccFree);
 }
 
 template <int D, int N>
@@ -496,33 +603,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* s_abort = reinterpret_cast<volatile int*>(&bars[kSlotAbort]);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  const int H = p.b.H, h = blockIdx.x % H;
-  const BwdWork w = p.work[blockIdx.x / H];
-  const bool dq = w.kind == kBwdDQ;
-  const bool bidir = p.b.bidir != 0;
-  const BwdTiles seq = dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir)
-                          : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, bidir);
-  const int nt = w.hi - w.lo;
   constexpr int nA = C::kA, nB = C::kB;
 
   launch_dependents();
+  {  // the first item's entry, into the constant cache while the CTA sets up
+    const BwdWork& first = p.work[blockIdx.x / p.b.H];
+    asm volatile("" ::"r"(first.kind), "r"(first.start));
+  }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(B(kBarRes + s), dq && s == 1 ? kSoftmaxThreads / 32 : 1);
-      mbar_init(B(kBarS + s), 1);
-      mbar_init(B(kBarStats + s), 1);
-      mbar_init(B(kBarP + s), kSoftmaxThreads / 32);
-      mbar_init(B(kBarDS + s), kSoftmaxThreads / 32);
+    constexpr int kWarps = kSoftmaxThreads / 32;
+    for (int s = 0; s < kBarEnd + 1; ++s) {
+      const bool per_warp = s == kBarRows || s == kBarAccFree || s == kBarP || s == kBarP + 1 || s == kBarDS ||
+                            s == kBarDS + 1 || s == kBarRead || s == kBarStatsFree || s == kBarStatsFree + 1;
+      // the roles that read an item's number: MMA, statistics, softmax
+      mbar_init(B(s), per_warp ? kWarps : s == kBarItemFree || s == kBarItemFree + 1 ? kWarps + 2 : 1);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(B(kBarAFull + s), 1);
-      mbar_init(B(kBarAFree + s), 1);
-      mbar_init(B(kBarBFull + s), 1);
-      mbar_init(B(kBarBFree + s), 1);
-    }
-    mbar_init(B(kBarDP), 1);
-    mbar_init(B(kBarRead), kSoftmaxThreads / 32);
-    mbar_init(B(kBarFinal), 1);
     *s_abort = (sbase & 1023) != 0;
     fence_barrier_init();
   }
@@ -537,134 +632,182 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
+  Item item;
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     if (lane == 0) {
+      auto wait = [&](int slot, int phase) { return wait_phase(bar0, slot, phase); };
       auto load = [&](uint32_t dst, const CUtensorMap* map, int tile, uint32_t bar) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
         for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, h, w.start + tile * kTile, bar);
+          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, item.h, item.w.start + tile * kTile, bar);
       };
-      const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
-      const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
-      if (dq) {
-        mbar_arrive_expect_tx(B(kBarRes), 2 * C::kTileBytes);
-        for (int x = 0; x < C::kBoxes; ++x) {
-          tma_load_3d(smRes + x * kBoxBytes, &p.tmQ, kBox * x, h, w.start + w.tile * kTile, B(kBarRes));
-          tma_load_3d(smRes + C::kTileBytes + x * kBoxBytes, &p.tmG, kBox * x, h, w.start + w.tile * kTile, B(kBarRes));
-        }
-      } else {
-        load(smRes, &p.tmK, w.tile, B(kBarRes));
-      }
-      int a = 0, b = 0;  // tiles issued on each ring
+      int a = 0, b = 0, r = 0;   // tiles issued on each ring, items whose own tiles were
+      int T = 0, U = 0, kq = 0;  // as Item's
       bool ok = true;
-      for (int j = 0; j < nt && ok; ++j) {
-        const int tile = seq.at(w.lo + j);
-        ok = !*s_abort && mbar_wait_bounded(B(kBarAFree + j % nA), ((j / nA) & 1) ^ 1);
+      for (int id = blockIdx.x; ok;) {
+        const int k = item.k;
+        ok = wait(kBarItemFree + (k & 1), (k >> 1) + 1);
         if (!ok) break;
-        load(smA + (j % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + j % nA));
-        ++a;
-        if (j == 0 && !dq) load(smRes + C::kTileBytes, &p.tmV, w.tile, B(kBarRes + 1));
-        ok = !*s_abort && mbar_wait_bounded(B(kBarBFree + j % nB), ((j / nB) & 1) ^ 1);
-        if (!ok) break;
-        load(smB + (j % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + j % nB));
-        ++b;
+        if (id >= p.n_items) id = -1;
+        const uint32_t slot = Item::slot(bar0, k);
+        st_shared(slot, id);
+        if (id >= 0) {
+          item.decode(p, id);
+          st_shared(slot + 4, T);
+          st_shared(slot + 8, U);
+          st_shared(slot + 12, kq);
+          st_shared(slot + 16, item.w.len);
+          st_shared(slot + 20, item.w.ref);
+        }
+        mbar_arrive(B(kBarItem + (k & 1)));
+        if (id < 0) break;
+        const bool dq = item.dq;
+        const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
+        const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
+        for (int j = 0; j < item.nt; ++j) {
+          const int tile = item.seq.at(item.w.lo + j);
+          ok = wait(kBarAFree + a % nA, a / nA + 1);
+          if (!ok) break;
+          load(smA + (a % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + a % nA));
+          ++a;
+          if (j == 0) {
+            ok = k == 0 || wait(kBarResFree, k - 1);
+            if (!ok) break;
+            load(smRes, dq ? &p.tmQ : &p.tmK, item.w.tile, B(kBarRes));
+            load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, item.w.tile, B(kBarRes + 1));
+            ++r;
+          }
+          ok = wait(kBarBFree + b % nB, b / nB + 1);
+          if (!ok) break;
+          load(smB + (b % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + b % nB));
+          ++b;
+        }
+        T += item.nt;
+        if (dq) ++kq;
+        else U += item.nt;
+        ++item.k;
+        // The counter is zeroed by the kernel before this one.
+        dependency_wait();
+        id = (int)gridDim.x + atomicAdd(p.b.counter, 1);
       }
       if (!ok) *s_abort = 1;
       // drain: every issued copy has landed before the CTA may exit
-      mbar_wait_bounded(B(kBarRes), 0);
-      if (!dq && a > 0) mbar_wait_bounded(B(kBarRes + 1), 0);
+      if (r > 0) {
+        mbar_wait_bounded(B(kBarRes), (r - 1) & 1);
+        mbar_wait_bounded(B(kBarRes + 1), (r - 1) & 1);
+      }
       for (int j = max(0, a - nA); j < a; ++j) mbar_wait_bounded(B(kBarAFull + j % nA), (j / nA) & 1);
       for (int j = max(0, b - nB); j < b; ++j) mbar_wait_bounded(B(kBarBFull + j % nB), (j / nB) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    {
-      const int lead = lane == 0;
-      // (every lane of the warp answers the same)
-      auto wait = [&](int slot, int phase) {
-        return __all_sync(0xffffffffu, wait_phase(B(slot), phase, s_abort)) != 0;
-      };
-      auto tileA = [&](int j) { return smA + (j % nA) * C::kTileBytes; };
-      auto tileB = [&](int j) { return smB + (j % nB) * C::kTileBytes; };
-      bool ok;
-      if (dq) {
+    const int lead = lane == 0;
+    // (every lane of the warp answers the same)
+    auto wait = [&](int slot, int phase) {
+      return __all_sync(0xffffffffu, wait_phase(bar0, slot, phase)) != 0;
+    };
+    bool ok = true;
+    while (ok && item.next(bar0, p)) {
+      const int nt = item.nt, T = item.T, U = item.U, k = item.k;
+      // stages of ring A: of the next S and of the next gradient product; of ring B: of the next dP
+      int sa = T % nA, pa = T / nA & 1, ga = sa, sb = T % nB, pb = T / nB & 1, gb = sb;
+      auto step = [](int& s, int n) { s = s + 1 == n ? 0 : s + 1; };
+      // the accumulators of the item before have been read
+      auto acc_free = [&](int j) { return j > 0 || k == 0 || wait(kBarAccFree, k - 1); };
+      if (item.dq) {
         const uint32_t S = tmem, dP = tmem + 128, dQ = tmem + 384, aQ = tmem + kColA, aG = aQ + D / 2;
         auto scores = [&](int j) -> bool {  // S(j) = Q K_j^T
-          if (!wait(kBarAFull + j % nA, j / nA)) return false;
+          if (!wait(kBarAFull + sa, pa)) return false;
           tc_fence_after();
-          mma_scores_ta<D>(lead, S, aQ, tileA(j));
-          commit(lead, B(kBarS + (j & 1)));
+          mma_scores_ta<D>(lead, S, aQ, smA + sa * C::kTileBytes);
+          commit(lead, B(kBarS + ((T + j) & 1)));
+          step(sa, nA);
+          pa ^= sa == 0;
           return true;
         };
         auto dprob = [&](int j) -> bool {  // dP(j) = dO V_j^T
-          if (!wait(kBarBFull + j % nB, j / nB)) return false;
+          if (!wait(kBarBFull + sb, pb)) return false;
           tc_fence_after();
-          mma_scores_ta<D>(lead, dP, aG, tileB(j));
+          mma_scores_ta<D>(lead, dP, aG, smB + sb * C::kTileBytes);
           commit(lead, B(kBarDP));
-          commit(lead, B(kBarBFree + j % nB));
+          commit(lead, B(kBarBFree + sb));
+          step(sb, nB);
+          pb ^= sb == 0;
           return true;
         };
-        ok = wait(kBarRes + 1, 0) && scores(0) && dprob(0);
+        ok = wait(kBarRows, item.kq);
+        if (ok && lane == 0) mbar_arrive(B(kBarResFree));
+        ok = ok && scores(0) && dprob(0);
         for (int j = 0; j < nt && ok; ++j) {
-          if (j + 1 < nt) ok = wait(kBarRead, j) && scores(j + 1);
-          ok = ok && wait(kBarDS + (j & 1), j >> 1);
+          if (j + 1 < nt) ok = wait(kBarRead, T + j) && scores(j + 1);
+          ok = ok && wait(kBarDS + ((T + j) & 1), (T + j) >> 1) && acc_free(j);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(lead, dQ, dP, tileA(j), j > 0);
-          commit(lead, B(kBarAFree + j % nA));
+          mma_grad<D>(lead, dQ, dP, smA + ga * C::kTileBytes, j > 0);
+          commit(lead, B(kBarAFree + ga));
+          step(ga, nA);
           if (j + 1 < nt) ok = dprob(j + 1);
         }
       } else {
         const uint32_t dV = tmem + 256, dK = tmem + 384;
         auto scores = [&](int j) -> bool {  // S(j)^T = K Q_j^T
-          if (!wait(kBarAFull + j % nA, j / nA)) return false;
+          if (!wait(kBarAFull + sa, pa)) return false;
           tc_fence_after();
-          mma_scores<D>(lead, tmem + (j & 1) * 128, smRes, tileA(j));
-          commit(lead, B(kBarS + (j & 1)));
+          mma_scores<D>(lead, tmem + (j & 1) * 128, smRes, smA + sa * C::kTileBytes);
+          commit(lead, B(kBarS + ((T + j) & 1)));
+          step(sa, nA);
+          pa ^= sa == 0;
           return true;
         };
         auto dprob = [&](int j) -> bool {  // dP(j)^T = V dO_j^T
-          if (!wait(kBarBFull + j % nB, j / nB)) return false;
+          if (!wait(kBarBFull + sb, pb)) return false;
           tc_fence_after();
-          mma_scores<D>(lead, tmem + ((j & 1) ^ 1) * 128, smRes + C::kTileBytes, tileB(j));
+          mma_scores<D>(lead, tmem + ((j & 1) ^ 1) * 128, smRes + C::kTileBytes, smB + sb * C::kTileBytes);
           commit(lead, B(kBarDP));
+          if (j == nt - 1) commit(lead, B(kBarResFree));
+          step(sb, nB);
+          pb ^= sb == 0;
           return true;
         };
-        ok = wait(kBarRes, 0) && scores(0) && wait(kBarRes + 1, 0) && dprob(0);
+        ok = wait(kBarRes, k) && scores(0) && wait(kBarRes + 1, k) && dprob(0);
         for (int j = 0; j < nt && ok; ++j) {
-          ok = wait(kBarP + (j & 1), j >> 1);
+          ok = wait(kBarP + ((U + j) & 1), (U + j) >> 1) && acc_free(j);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(lead, dV, tmem + (j & 1) * 128, tileB(j), j > 0);
-          commit(lead, B(kBarBFree + j % nB));
-          if (j + 1 < nt) ok = wait(kBarRead, j) && scores(j + 1);
-          ok = ok && wait(kBarDS + (j & 1), j >> 1);
+          mma_grad<D>(lead, dV, tmem + (j & 1) * 128, smB + gb * C::kTileBytes, j > 0);
+          commit(lead, B(kBarBFree + gb));
+          step(gb, nB);
+          if (j + 1 < nt) ok = wait(kBarRead, T + j) && scores(j + 1);
+          ok = ok && wait(kBarDS + ((T + j) & 1), (T + j) >> 1);
           if (!ok) break;
           tc_fence_after();
-          mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + kCols / 2, tileA(j), j > 0);
-          commit(lead, B(kBarAFree + j % nA));
+          mma_grad<D>(lead, dK, tmem + (j & 1) * 128 + kCols / 2, smA + ga * C::kTileBytes, j > 0);
+          commit(lead, B(kBarAFree + ga));
+          step(ga, nA);
           if (j + 1 < nt) ok = dprob(j + 1);
         }
       }
-      if (!ok) *s_abort = 1;
-      // every MMA issued by this thread has completed before TMEM is read or freed
       commit(lead, B(kBarFinal));
-      mbar_wait_bounded(B(kBarFinal), 0);
+      item.done(bar0, lane);
     }
+    if (!ok) *s_abort = 1;
+    // every MMA issued by this thread has completed before TMEM is freed
+    commit(lead, B(kBarEnd));
+    mbar_wait_bounded(B(kBarEnd), 0);
   } else if (warp == 2) {
     // -------------------------------------------------- row statistics
-    if (!dq) {
-      dependency_wait();
-      for (int j = 0; j < nt; ++j) {
-        const int s = j & 1;
-        // the softmax has read the statistics of tile j - 2 once its dS is there
-        const bool free = j < 2 || (!*s_abort && mbar_wait_bounded(B(kBarDS + s), ((j - 2) >> 1) & 1));
-        if (!__all_sync(0xffffffffu, free)) break;
+    dependency_wait();
+    bool ok = true;
+    while (ok && item.next(bar0, p)) {
+      for (int j = 0; !item.dq && j < item.nt; ++j) {
+        const int u = item.U + j, s = u & 1;
+        ok = __all_sync(0xffffffffu, wait_phase(bar0, kBarStatsFree + s, (u >> 1) + 1));
+        if (!ok) break;
         // rows past the document's end are another's, or padding of the array
-        const float2* src = p.b.stats + (size_t)h * p.b.stat_stride + w.start + seq.at(w.lo + j) * kTile;
+        const float2* src = p.b.stats + (size_t)item.h * p.b.stat_stride + item.w.start + item.seq.at(item.w.lo + j) * kTile;
         float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -675,11 +818,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(B(kBarStats + s));
       }
+      item.done(bar0, lane);
     }
   } else if (warp >= kSoftmaxWarp) {
-    const Ctx c{p, w, seq, smem, bar0, tmem, s_abort, h};
-    if (dq) softmax_warps<D, true>(c);
-    else softmax_warps<D, false>(c);
+    bool ok = true;
+    for (int k = 0;; ++k) {
+      if (!Item::announced(bar0, k)) break;
+      const int id = k == 0 ? (int)blockIdx.x : ld_shared(Item::slot(bar0, k));
+      if (id < 0) break;
+      if (p.work[id / p.b.H].kind == kBwdDQ) softmax_item<D, true>(bar0, tmem, p, k, ok);
+      else softmax_item<D, false>(bar0, tmem, p, k, ok);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(B(kBarItemFree + (k & 1)));
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -697,11 +848,16 @@ cudaError_t launch(const BwdTcParams& common, const BwdWork* work, int n_work, c
   if (e != cudaSuccess) return e;
   BwdLaunch<BwdTcParams, N> p;
   static_cast<BwdTcParams&>(p) = common;
+  int dev = 0, sms = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   for (int w0 = 0; w0 < n_work; w0 += N) {
     const int m = std::min(N, n_work - w0);
     std::copy_n(work + w0, m, p.work);
-    e = launch_dependent(backward_tc_kernel<D, N>, m * p.b.H, kThreads, Cfg<D>::kSmBytes, stream, p);
+    p.n_items = m * p.b.H;
+    e = launch_dependent(backward_tc_kernel<D, N>, std::min(p.n_items, sms), kThreads, Cfg<D>::kSmBytes, stream, p);
     if (e != cudaSuccess) return e;
+    ++p.b.counter;
   }
   return cudaSuccess;
 }
