@@ -278,10 +278,15 @@ __device__ __forceinline__ float2 ld_shared2(uint32_t addr) {
   return v;
 }
 
-// A bounded wait (bar0: the barriers' base) that ends early once the CTA has given up.
+// A bounded wait (bar0: the barriers' base) that ends early once the CTA has
+// given up.  What follows a failed first try is out of line: inlined at every
+// wait it made up much of the kernel's code, which a launch fetches cold.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, uint32_t abort) {
+  return !ld_shared(abort) && mbar_wait_bounded(bar, parity);
+}
 __device__ __forceinline__ bool wait_phase(uint32_t bar0, int slot, int phase) {
   const uint32_t bar = bar0 + 8u * slot;
-  return mbar_try_wait(bar, phase & 1) || (!ld_shared(bar0 + 8u * kSlotAbort) && mbar_wait_bounded(bar, phase & 1));
+  return mbar_try_wait(bar, phase & 1) || wait_on(bar, phase & 1, bar0 + 8u * kSlotAbort);
 }
 
 // The item that a role works on.  What the CTA did before it comes from the
