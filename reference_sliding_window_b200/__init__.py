@@ -577,23 +577,31 @@ class Rotary:
             k = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
         else:
             q, k = (out, None) if K is None else out
-        index = Q.get_device()
+        index, d = Q.get_device(), self.d
         pos = None
         if positions is not None:
             if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.dim() == 1
                     and positions.shape[0] == rows and positions.get_device() == index and positions.is_contiguous()):
                 _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
             pos = positions.data_ptr()
-        sq, sqo = self._stride("Q", Q, rows, Q, index), self._stride("out of Q", q, rows, Q, index)
-        if q.shape != shape:
-            raise ValueError(f"out of Q has shape {tuple(q.shape)}, expected {tuple(shape)}")
+        sq = self._stride("Q", Q, rows, Q, index)
+        if out is None:
+            sqo = shape[1] * d
+        else:
+            sqo = self._stride("out of Q", q, rows, Q, index)
+            if q.shape != shape:
+                raise ValueError(f"out of Q has shape {tuple(q.shape)}, expected {tuple(shape)}")
         if K is None:
             keys = (None, 0, 0, None, 0)
         else:
-            keys = (K.data_ptr(), self._stride("K", K, rows, Q, index), K.shape[1], k.data_ptr(),
-                    self._stride("out of K", k, rows, Q, index))
-            if k.shape != K.shape:
-                raise ValueError(f"out of K has shape {tuple(k.shape)}, expected {tuple(K.shape)}")
+            sk, heads = self._stride("K", K, rows, Q, index), K.shape[1]
+            if out is None:
+                sko = heads * d
+            else:
+                sko = self._stride("out of K", k, rows, Q, index)
+                if k.shape != K.shape:
+                    raise ValueError(f"out of K has shape {tuple(k.shape)}, expected {tuple(K.shape)}")
+            keys = (K.data_ptr(), sk, heads, k.data_ptr(), sko)
         _call(index, self._apply, self._ref, Q.data_ptr(), sq, shape[1], q.data_ptr(), sqo, *keys, pos, int(first), rows,
               dt, 1 if inverse else 0, _stream_ptr(Q.device))
         return q if K is None else (q, k)

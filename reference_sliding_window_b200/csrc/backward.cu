@@ -37,10 +37,12 @@ Plan make_plan(int size, const int32_t* cu, const int32_t* refs, int n_docs, int
         total += item_cost(kind, tiles);
       }
   }
-  // An item much longer than the SMs' equal share would end last, alone: it
-  // is cut into shares of the tile sequence whose partial sums a second kernel
-  // adds in order.
-  const long long limit = std::max<long long>(total * H / kSMs / 3, 60);
+  // An item longer than the SMs' equal share would end last, alone: it is cut
+  // into shares of the tile sequence whose partial sums a second kernel adds in
+  // order.  Shorter limits cost more in partials than they even out (2592 + 4001
+  // rows, d = 128: 10 heads 255 us uncut against 283 with limits of a third of
+  // the share; one head of 288 + 19712 rows 62 us cut against 113 uncut).
+  const long long limit = std::max<long long>(total * H / kSMs, 60);
   std::vector<BwdWork> cut;
   for (const BwdWork& w : plan.work) {
     const long long cost = item_cost(w.kind, w.hi);
@@ -114,36 +116,41 @@ struct JoinParams {
   BwdJoin join[kMaxJoin];
 };
 
-// Adds a split tile's partials in order.  One CTA per (tile, head).
+// Adds a split tile's partials in order.  One CTA per (tile, head, gradient and
+// slice of the tile's rows): few tiles are split, so a tile has many CTAs.
+constexpr int kJoinSlices = 8;
 template <typename T>
 __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
   dependency_wait();
   const BackwardParams& b = p.b;
-  const BwdJoin w = p.join[blockIdx.x / b.H];
-  const int h = blockIdx.x % b.H;
+  const int which = blockIdx.x & 1, slice = (blockIdx.x >> 1) % kJoinSlices;
+  const int tile_head = blockIdx.x / (2 * kJoinSlices);
+  const BwdJoin w = p.join[tile_head / b.H];
+  if (which == 1 && w.kind == kBwdDQ) return;
+  const int h = tile_head % b.H;
   const int tile_elems = p.size * b.D;
-  const int row0 = w.tile * p.size;
-  const int rows = min(p.size, w.len - row0);
+  const int first = w.tile * p.size, slice_rows = p.size / kJoinSlices;
+  const int rows = min(slice_rows, w.len - first - slice * slice_rows);  // may be <= 0
   const size_t stride = (size_t)b.H * 2 * tile_elems;
-  for (int which = 0; which < (w.kind == kBwdDQ ? 1 : 2); ++which) {
-    T* grad = static_cast<T*>(w.kind == kBwdDQ ? b.dQ : which == 0 ? b.dV : b.dK);
-    const float mul = w.kind == kBwdDKV && which == 0 ? 1.f : b.scale;
-    const float* part = b.partials + ((size_t)w.part * b.H + h) * 2 * tile_elems + which * tile_elems;
-    for (int c = threadIdx.x * 4; c < rows * b.D; c += 256 * 4) {
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < w.n_parts; ++s) {
-        const float4 x = *reinterpret_cast<const float4*>(part + s * stride + c);
-        sum.x += x.x;
-        sum.y += x.y;
-        sum.z += x.z;
-        sum.w += x.w;
-      }
-      T* dst = grad + ((size_t)(w.start + row0 + c / b.D) * b.H + h) * b.D + c % b.D;
-      store_elem(dst, sum.x * mul);
-      store_elem(dst + 1, sum.y * mul);
-      store_elem(dst + 2, sum.z * mul);
-      store_elem(dst + 3, sum.w * mul);
+  T* grad = static_cast<T*>(w.kind == kBwdDQ ? b.dQ : which == 0 ? b.dV : b.dK) +
+            ((size_t)(w.start + first + slice * slice_rows) * b.H + h) * b.D;
+  const float mul = w.kind == kBwdDKV && which == 0 ? 1.f : b.scale;
+  const float* part = b.partials + (((size_t)w.part * b.H + h) * 2 + which) * tile_elems + slice * slice_rows * b.D;
+  for (int c = threadIdx.x * 4; c < rows * b.D; c += 256 * 4) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < w.n_parts; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(part + s * stride + c);
+      sum.x += x.x;
+      sum.y += x.y;
+      sum.z += x.z;
+      sum.w += x.w;
     }
+    T* dst = grad + (size_t)(c / b.D) * b.H * b.D + c % b.D;
+    store_elem(dst, sum.x * mul);
+    store_elem(dst + 1, sum.y * mul);
+    store_elem(dst + 2, sum.z * mul);
+    store_elem(dst + 3, sum.w * mul);
   }
 }
 
@@ -178,8 +185,8 @@ cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStr
   for (size_t w0 = 0; w0 < plan.joins.size(); w0 += kMaxJoin) {
     const int m = (int)std::min<size_t>(kMaxJoin, plan.joins.size() - w0);
     std::copy_n(plan.joins.begin() + w0, m, j.join);
-    e = launch_dependent(elem == kF32 ? backward_join_kernel<float> : backward_join_kernel<__nv_bfloat16>, m * p.H, 256, 0,
-                         stream, j);
+    e = launch_dependent(elem == kF32 ? backward_join_kernel<float> : backward_join_kernel<__nv_bfloat16>, m * p.H * 2 * kJoinSlices,
+                         256, 0, stream, j);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

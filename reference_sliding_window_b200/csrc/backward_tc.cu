@@ -514,6 +514,10 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
 #pragma unroll
     for (int q = 0; q < kPer; ++q) tmem_ld_frag(tP + kCols * q, dp + kCols * q);
     tmem_wait_ld();
+    if (past_end) {  // a masked weight of 0 times a NaN of another document's row
+#pragma unroll
+      for (int e = 0; e < kPer * kCols; ++e) dp[e] = x[e] == 0.f ? 0.f : dp[e];
+    }
     if (!DQ) {
       tc_fence_before();
       arrive(kBarRead);
@@ -530,8 +534,6 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
           addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
         }
       }
-      // a masked weight of 0 times a NaN of another document's row
-      if (past_end) mask(x + kCols * q, q, ld_shared(slot + 16), ld_shared(slot + 20));
       tmem_st_frag((DQ ? tP : tS + kCols / 2) + kCols * q, x + kCols * q);
     }
     tmem_wait_st();
@@ -811,12 +813,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int u = item.U + j, s = u & 1;
         ok = __all_sync(0xffffffffu, wait_phase(bar0, kBarStatsFree + s, (u >> 1) + 1));
         if (!ok) break;
-        // rows past the document's end are another's, or padding of the array
-        const float2* src = p.b.stats + (size_t)item.h * p.b.stat_stride + item.w.start + item.seq.at(item.w.lo + j) * kTile;
+        // (rows past the document's end are another's: zeros in their place)
+        const int q0 = item.seq.at(item.w.lo + j) * kTile;
+        const float2* src = p.b.stats + (size_t)item.h * p.b.stat_stride + item.w.start + q0;
         float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = src[lane + 32 * i];
+          const float2 v = q0 + lane + 32 * i < item.w.len ? src[lane + 32 * i] : make_float2(0.f, 0.f);
           dst[lane + 32 * i] = v.x;
           dst[kTile + lane + 32 * i] = v.y;
         }

@@ -53,11 +53,19 @@ template <typename T, bool VEC, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p, int units, int groups) {
   constexpr int V = Vec16<T>::N;
   constexpr int kPairs = !VEC ? 1 : INTER ? V / 2 : V;
-  const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
-  const int u = (int)(idx % units);
-  const long long rg = idx / units;
-  const int g = (int)(rg % groups);
-  const long long row = rg / groups;
+  int u, g;
+  long long row;
+  if (gridDim.x <= 0xffffffffu / kThreads) {  // (a 64-bit division costs as much as a head's turn)
+    const unsigned idx = blockIdx.x * kThreads + threadIdx.x, rg = idx / (unsigned)units;
+    u = (int)(idx - rg * (unsigned)units);
+    row = rg / (unsigned)groups;
+    g = (int)(rg - (unsigned)row * (unsigned)groups);
+  } else {
+    const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x, rg = idx / units;
+    u = (int)(idx % units);
+    row = rg / groups;
+    g = (int)(rg % groups);
+  }
   dependency_wait();
   if (row >= p.rows) return;
   const int dim = p.plan.dim, half = dim / 2;
@@ -72,42 +80,71 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     for (int i = 0; i < kPairs; ++i) t[i] = turn_at(pos, p.plan.turn[u * kPairs + i], p.plan.mscale, p.sign);
   }
   const int heads = p.x[0].heads + p.x[1].heads;
-#pragma unroll 4
-  for (int h = g; h < heads; h += groups) {
-    const bool second = h >= p.x[0].heads;
-    const RotaryTensor& x = p.x[second];
-    const int hh = second ? h - p.x[0].heads : h;
-    const T* in = static_cast<const T*>(x.in) + row * x.in_stride + (long long)hh * p.plan.d;
-    T* out = static_cast<T*>(x.out) + row * x.out_stride + (long long)hh * p.plan.d;
+  // In place, a load may not pass a store as far as the compiler knows, so a
+  // thread loads kBatch heads before it stores any (each element has one reader
+  // and writer).
+  constexpr int kBatch = 4;
+  for (int h0 = g; h0 < heads; h0 += kBatch * groups) {
+    const T* in[kBatch];
+    T* out[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int h = min(h0 + j * groups, heads - 1);
+      const bool second = h >= p.x[0].heads;
+      const RotaryTensor& x = p.x[second];
+      const long long at = (long long)(second ? h - p.x[0].heads : h) * p.plan.d;
+      in[j] = static_cast<const T*>(x.in) + row * x.in_stride + at;
+      out[j] = static_cast<T*>(x.out) + row * x.out_stride + at;
+    }
     if constexpr (VEC) {
-      const uint4 a = *reinterpret_cast<const uint4*>(in + e0);
-      if (!turns) {
-        *reinterpret_cast<uint4*>(out + e0) = a;
-        continue;
-      }
-      float f[V];
-      Vec16<T>::unpack(a, f);
-      if constexpr (INTER) {
+      uint4 a[kBatch], b[kBatch];
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) rotate(f[2 * i], f[2 * i + 1], t[i]);
-      } else {
-        float f1[V];
-        Vec16<T>::unpack(*reinterpret_cast<const uint4*>(in + e1), f1);
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j * groups < heads) {
+          a[j] = *reinterpret_cast<const uint4*>(in[j] + e0);
+          if (!INTER && turns) b[j] = *reinterpret_cast<const uint4*>(in[j] + e1);
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i) rotate(f[i], f1[i], t[i]);
-        *reinterpret_cast<uint4*>(out + e1) = pack16<T>(f1);
-      }
-      *reinterpret_cast<uint4*>(out + e0) = pack16<T>(f);
-    } else if (turns) {
-      const int ea = e0, eb = INTER ? e0 + 1 : e1;
-      float x0 = load_elem(in + ea), x1 = load_elem(in + eb);
-      rotate(x0, x1, t[0]);
-      store_elem(out + ea, x0);
-      store_elem(out + eb, x1);
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j * groups < heads) {
+          if (turns) {
+            float f[V];
+            Vec16<T>::unpack(a[j], f);
+            if constexpr (INTER) {
+#pragma unroll
+              for (int i = 0; i < kPairs; ++i) rotate(f[2 * i], f[2 * i + 1], t[i]);
+            } else {
+              float f1[V];
+              Vec16<T>::unpack(b[j], f1);
+#pragma unroll
+              for (int i = 0; i < V; ++i) rotate(f[i], f1[i], t[i]);
+              *reinterpret_cast<uint4*>(out[j] + e1) = pack16<T>(f1);
+            }
+            a[j] = pack16<T>(f);
+          }
+          *reinterpret_cast<uint4*>(out[j] + e0) = a[j];
+        }
     } else {
-      const T a = in[e0], b = in[e0 + 1];
-      out[e0] = a;
-      out[e0 + 1] = b;
+      const int eb = turns && !INTER ? e1 : e0 + 1;
+      T a[kBatch], b[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j * groups < heads) {
+          a[j] = in[j][e0];
+          b[j] = in[j][eb];
+        }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (h0 + j * groups < heads) {
+          if (turns) {
+            float x0 = load_elem(&a[j]), x1 = load_elem(&b[j]);
+            rotate(x0, x1, t[0]);
+            store_elem(&a[j], x0);
+            store_elem(&b[j], x1);
+          }
+          out[j][e0] = a[j];
+          out[j][eb] = b[j];
+        }
     }
   }
 }

@@ -112,6 +112,40 @@ def test_few_heads_and_long_sequences_split_their_sums(dtype, d):
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_pack_of_very_many_documents(dtype, d):
+    """More work entries than one launch takes: each document is at least a query tile and a key tile."""
+    rng = np.random.default_rng(3)
+    cu, refs = [0], []
+    for size in rng.integers(1, 7, size=700).tolist() + [200]:
+        refs.append(int(rng.integers(0, size + 1)))
+        cu.append(cu[-1] + size)
+    _check(*_inputs(cu[-1], 1, d, dtype, seed=17), cu, refs, 3, bidir=True)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128)])
+def test_two_calls_at_once(dtype, d):
+    """Calls on two streams that overlap on the GPU, each with its own workspace."""
+    args = []
+    for seed in (51, 52):
+        dO, Q, K, V = _inputs(2000, 4, d, dtype, seed=seed)
+        O, lse = masked_forward(Q, K, V, L_m=700, n=64, return_lse=True)
+        args.append((dO, Q, K, V, O, lse))
+    want = [masked_backward(*a, L_m=700, n=64) for a in args]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(masked_backward(*args[i], L_m=700, n=64))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for x, y in zip(g, want[i]):
+                assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
 def test_gradient_repeats_bit_for_bit_and_per_document(dtype, d):
     cu, refs, n = [0, 700, 1001], [288, 30], 128
     dO, Q, K, V = _inputs(cu[-1], 3, d, dtype, seed=12)
