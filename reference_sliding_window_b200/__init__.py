@@ -21,6 +21,7 @@ inside RSWA.append_decode, RSWA.prefill and masked_attention (rotary=...).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import Optional, Sequence
 
 import numpy as np
@@ -393,7 +394,20 @@ def _pack_args(Q: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[in
     n_docs = len(ref_lens)
     if len(cu_seqlens) != n_docs + 1 or int(cu_seqlens[-1]) != L:
         raise ValueError("cu_seqlens must have len(ref_lens) + 1 entries ending at L")
-    return L, H, d, (C.c_int32 * (n_docs + 1))(*map(int, cu_seqlens)), (C.c_int32 * max(n_docs, 1))(*map(int, ref_lens))
+    return (L, H, d) + _documents(tuple(map(int, cu_seqlens)), tuple(map(int, ref_lens)))
+
+
+@functools.lru_cache(maxsize=64)
+def _documents(cu_seqlens: tuple, ref_lens: tuple) -> tuple:
+    """The documents as host arrays for the library, which only reads them."""
+    return (C.c_int32 * len(cu_seqlens))(*cu_seqlens), (C.c_int32 * max(len(ref_lens), 1))(*ref_lens)
+
+
+@functools.lru_cache(maxsize=64)
+def _backward_workspace_bytes(cu_seqlens: tuple, ref_lens: tuple, n: int, H: int, d: int, dtype: int, flags: int) -> int:
+    """A pure function of the sizes, that plans the whole call: remembered."""
+    return _native.lib().rswa_masked_backward_workspace_bytes(*_documents(cu_seqlens, ref_lens), len(ref_lens), n, H, d,
+                                                              dtype, flags)
 
 
 def _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, out, bidir_prefix):
@@ -504,7 +518,7 @@ def masked_backward_varlen(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V
     lib = _native.lib()
     dt, docs, n = _DT[Q.dtype], len(ref_lens), int(n)
     flags = _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0
-    ws_bytes = lib.rswa_masked_backward_workspace_bytes(cu, refs, docs, n, H, d, dt, flags)
+    ws_bytes = _backward_workspace_bytes(tuple(map(int, cu_seqlens)), tuple(map(int, ref_lens)), n, H, d, dt, flags)
     # 0 bytes: arguments that the call itself reports
     ws = Q.new_empty((max(ws_bytes, 16),), dtype=torch.uint8)
     _call(index, lib.rswa_masked_backward, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
@@ -565,6 +579,8 @@ class Rotary:
         themselves.  Returns Q's result, or the pair."""
         if not isinstance(Q, torch.Tensor):
             raise TypeError("Q must be a torch.Tensor")
+        if K is not None and not isinstance(K, torch.Tensor):
+            raise TypeError("K must be a torch.Tensor")
         if not Q.is_cuda:
             raise ValueError(f"Q is on {Q.device}, expected a CUDA device")
         dt = _DT.get(Q.dtype)
@@ -573,8 +589,10 @@ class Rotary:
         shape = Q.shape
         rows = shape[0] if len(shape) == 3 else 0
         if out is None:
-            q = torch.empty_like(Q, memory_format=torch.contiguous_format)
-            k = None if K is None else torch.empty_like(K, memory_format=torch.contiguous_format)
+            # (empty_like of a contiguous tensor is, and is the cheaper call)
+            q = torch.empty_like(Q) if Q.is_contiguous() else torch.empty_like(Q, memory_format=torch.contiguous_format)
+            k = (None if K is None else torch.empty_like(K) if K.is_contiguous()
+                 else torch.empty_like(K, memory_format=torch.contiguous_format))
         else:
             q, k = (out, None) if K is None else out
         index, d = Q.get_device(), self.d
