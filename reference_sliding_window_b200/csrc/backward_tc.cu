@@ -3,10 +3,13 @@
 // accumulation.  The formulas, the mask and the work items are in backward.h.
 //
 // One CTA per SM, which takes (work item, head) pairs off a counter, heaviest
-// first; tiles of 128 queries x 128 keys.  Bound: the
-// tensor pipe (4 tile products per key tile and query tile in a dK, dV item, 3
-// in a dQ item), with the exponentials and the products' operand reads from
-// shared memory close behind.
+// first; tiles of 128 queries x 128 keys.  Bound: the tensor pipe (4 tile
+// products per tile pair in a dK, dV item, 3 in a dQ item) and the operands it
+// reads from shared memory, with the exponentials close behind.  Measured at
+// 12832 + 19936 rows, 10 heads, d = 128: 3320 cycles a tile pair in dK, dV
+// items and 2440 in dQ items, of 2048 and 1536 at the MMA's rate; 5.0 ms, 875
+// TFLOP/s of the five products that the gradient cannot do without (5.6 ms,
+// 780 TFLOP/s, once the power limit has lowered the clock).
 //
 // * A dK, dV item keeps its K and V tiles in shared memory and streams Q and
 //   dO tiles.  S and dP are formed transposed (keys on TMEM lanes), so that P
@@ -21,8 +24,7 @@
 // * Warp 0 streams tiles with TMA (128-byte swizzle) through two rings, warp
 //   1 issues the MMAs, warp 2 stages the row statistics (dK, dV items, where
 //   they vary along a thread's columns), warps 3-18 are the softmax: four
-//   groups of 128 threads, one thread per TMEM lane and a quarter of its 128
-//   columns.
+//   groups of 128 threads, each for a quarter of the 128 score columns.
 // * Issue order of a dK, dV item, two score regions X, Y taking turns: S(i)
 //   in one, dP(i) in the other, then dV(i), which runs while the softmax reads
 //   dP(i), S(i+1) over the dP(i) just read, dK(i) and dP(i+1), under which it forms
@@ -56,8 +58,7 @@ namespace {
 constexpr int kThreads = 608;
 constexpr int kSoftmaxWarp = 3;
 constexpr int kSoftmaxThreads = 512;
-constexpr int kCols = 32;                          // score columns of a fragment block
-constexpr int kPer = 4 * 128 / kSoftmaxThreads;    // blocks of a softmax thread
+constexpr int kCols = 32;  // score columns of a softmax thread's fragments
 constexpr int kTmemCols = 512;
 constexpr uint32_t kColA = 256;  // dQ items: the rows of Q, then of dO, bf16 pairs
 
@@ -358,7 +359,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
   const int g = (warp - kSoftmaxWarp) >> 2;  // column quarter
   const int quarter = warp & 3;              // TMEM lanes 32 * quarter .. +31
   const int fg = lane >> 2, ft = lane & 3;   // the fragments' row and column pair
-  const int c0 = kPer * kCols * g;
+  const int c0 = kCols * g;
   const int own0 = w.tile * kTile + quarter * 32 + fg;  // the thread's local rows own0 + 8 i: queries (DQ) or keys
   const uint32_t base = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
   const float sl2 = p.scale_log2;
@@ -441,9 +442,9 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     const uint32_t tP = base + (DQ ? 128 : (odd ^ 1) * 128);
     const bool full = j >= f0 && j < f1;
     const uint32_t slot = Item::slot(bar0, item_k);
-    // Zeroes what the thread's rows do not see of block q.
-    auto mask = [&](float* y, int q, int len, int ref) {
-      const int x0 = o0 + c0 + kCols * q, n = min(p.b.n, len);  // (own + n stays small)
+    // Zeroes what the thread's rows do not see.
+    auto mask = [&](float* y, int len, int ref) {
+      const int x0 = o0 + c0, n = min(p.b.n, len);  // (own + n stays small)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int own = own0 + 8 * i;
@@ -460,21 +461,20 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     if (!DQ) wait(kBarStats + (iu & 1), iu >> 1);
     wait(kBarS + (it & 1), it >> 1);
     tc_fence_after();
-    float x[kPer * kCols];
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) tmem_ld_frag(tS + kCols * q, x + kCols * q);
+    float x[kCols];
+    tmem_ld_frag(tS, x);
     tmem_wait_ld();
     if (DQ) {
       tc_fence_before();
       arrive(kBarRead);
     }
 #pragma unroll
-    for (int k = 0; k < 4 * kPer; ++k) {
+    for (int k = 0; k < 4; ++k) {
       float2 l = make_float2(0.f, 0.f);
       if (!DQ) l = ld_shared2(st + 32 * k);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float* y = x + kCols * (k >> 2) + 16 * (i >> 1) + 2 * (i & 1) + 4 * (k & 3);
+        float* y = x + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
         fma2(y[0], y[1], sl2, DQ ? nlse[i] : l.x, DQ ? nlse[i] : l.y);
         y[0] = ex2(y[0]);
         y[1] = ex2(y[1]);
@@ -483,8 +483,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     bool past_end = false;
     if (!full) {
       const int len = ld_shared(slot + 16), ref = ld_shared(slot + 20);
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) mask(x + kCols * q, q, len, ref);
+      mask(x, len, ref);
       past_end = o0 + kTile > len;
       if (past_end) {  // rows of the streamed tiles past the document's end
         const int valid = len - o0;
@@ -502,40 +501,35 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
       }
     }
     if (!DQ) {
-#pragma unroll
-      for (int q = 0; q < kPer; ++q) tmem_st_frag(tS + kCols * q, x + kCols * q);
+      tmem_st_frag(tS, x);
       tmem_wait_st();
       tc_fence_before();
       arrive(kBarP + (iu & 1));
     }
     wait(kBarDP, it);
     tc_fence_after();
-    float dp[kPer * kCols];
-#pragma unroll
-    for (int q = 0; q < kPer; ++q) tmem_ld_frag(tP + kCols * q, dp + kCols * q);
+    float dp[kCols];
+    tmem_ld_frag(tP, dp);
     tmem_wait_ld();
     if (past_end) {  // a masked weight of 0 times a NaN of another document's row
 #pragma unroll
-      for (int e = 0; e < kPer * kCols; ++e) dp[e] = x[e] == 0.f ? 0.f : dp[e];
+      for (int e = 0; e < kCols; ++e) dp[e] = x[e] == 0.f ? 0.f : dp[e];
     }
     if (!DQ) {
       tc_fence_before();
       arrive(kBarRead);
     }
 #pragma unroll
-    for (int q = 0; q < kPer; ++q) {
+    for (int k = 0; k < 4; ++k) {
+      float2 d = make_float2(0.f, 0.f);
+      if (!DQ) d = ld_shared2(st + 4 * kTile + 32 * k);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 d = make_float2(0.f, 0.f);
-        if (!DQ) d = ld_shared2(st + 4 * (kTile + kCols * q) + 32 * k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = kCols * q + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
-          addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int e = 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
+        addmul2(x[e], x[e + 1], dp[e], dp[e + 1], DQ ? ndelta[i] : d.x, DQ ? ndelta[i] : d.y);
       }
-      tmem_st_frag((DQ ? tP : tS + kCols / 2) + kCols * q, x + kCols * q);
     }
+    tmem_st_frag(DQ ? tP : tS + kCols / 2, x);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
