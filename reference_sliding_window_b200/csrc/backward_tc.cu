@@ -112,7 +112,7 @@ enum : int {
   kBarStats = 34,     // 2 (dK, dV items)
   kBarStatsFree = 36, // 2
   kBarEnd = 38,
-  kSlotTmem = 39, kSlotAbort = 40, kSlotItem = 42  // 2 x 32 bytes: {number, T, U, kq, len, ref}
+  kSlotTmem = 39, kSlotAbort = 40, kSlotItem = 42  // 2 x 64 bytes: Item::Slot
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -273,6 +273,16 @@ __device__ __forceinline__ int ld_shared(uint32_t addr) {
 __device__ __forceinline__ void st_shared(uint32_t addr, int v) {
   asm volatile("st.volatile.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ void ld_shared4(uint32_t addr, int& a, int& b, int& c, int& d) {
+  asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, int a, int b, int c, int d) {
+  asm volatile("st.volatile.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ float2 ld_shared2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
@@ -290,67 +300,51 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar0, int slot, int phase) {
   return mbar_try_wait(bar, phase & 1) || wait_on(bar, phase & 1, bar0 + 8u * kSlotAbort);
 }
 
-// The item that a role works on.  What the CTA did before it comes from the
-// item's slot, so that no role carries it in registers from item to item.
+// What the producer announces of an item, four words at a time.  Every other
+// role reads it from here: working it out of the launch's list takes a role
+// hundreds of cycles, twice an item.
 struct Item {
-  BwdWork w;
-  BwdTiles seq;
-  int h, nt;
-  bool dq;
-  int T;      // tiles before it
-  int U;      // of them dK, dV items' tiles
-  int kq;     // dQ items before it
-  int k = 0;  // items before it
+  int number, T, U, kq;      // -1: no more; tiles before it; of them dK, dV items' tiles; dQ items before it
+  int start, len, ref, h;    // document and head
+  int tile, dq, nt, part;    // its tile, kind, tiles of its sequence, partial
+  int A, B0, lo, pad;        // tile lo + j of the sequence: its own number below A, B0 + (lo + j - A) from there on
 
-  // The next item, read by all lanes of a warp; false: there is none.
-  template <typename P>
-  __device__ __forceinline__ bool next(uint32_t bar0, const P& p) {
-    return announced(bar0, k) && read(bar0, p);
+  static __device__ __forceinline__ uint32_t slot(uint32_t bar0, int k) { return bar0 + 8u * kSlotItem + 64u * (k & 1); }
+  __device__ __forceinline__ int at(int j) const { return lo + j < A ? lo + j : B0 + lo + j - A; }
+
+  // Item k, read by all lanes of a warp; false: there is none.
+  __device__ __forceinline__ bool next(uint32_t bar0, int k) {
+    if (!__all_sync(0xffffffffu, wait_phase(bar0, kBarItem + (k & 1), k >> 1))) return false;
+    read(slot(bar0, k));
+    return number >= 0;
   }
-  template <typename P>
-  __device__ __forceinline__ bool read(uint32_t bar0, const P& p) {
-    const uint32_t s = slot(bar0, k);
-    const int id = k == 0 ? (int)blockIdx.x : ld_shared(s);
-    if (id < 0) return false;
-    T = k == 0 ? 0 : ld_shared(s + 4);
-    U = k == 0 ? 0 : ld_shared(s + 8);
-    kq = k == 0 ? 0 : ld_shared(s + 12);
-    decode(p, id);
-    return true;
+  __device__ __forceinline__ void read(uint32_t s) {
+    ld_shared4(s, number, T, U, kq);
+    ld_shared4(s + 16, start, len, ref, h);
+    ld_shared4(s + 32, tile, dq, nt, part);
+    ld_shared4(s + 48, A, B0, lo, pad);
   }
-  static __device__ __forceinline__ uint32_t slot(uint32_t bar0, int k) { return bar0 + 8u * kSlotItem + 32u * (k & 1); }
-  // Whether item k has been announced (by all lanes of a warp).  Every role knows the first.
-  static __device__ __forceinline__ bool announced(uint32_t bar0, int k) {
-    return k == 0 || __all_sync(0xffffffffu, wait_phase(bar0, kBarItem + (k & 1), k >> 1));
-  }
-  template <typename P>
-  __device__ __forceinline__ void decode(const P& p, int id) {
-    w = p.work[id / p.b.H];
-    h = id % p.b.H;
-    dq = w.kind == kBwdDQ;
-    seq = dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0)
-             : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0);
-    nt = w.hi - w.lo;
+  __device__ __forceinline__ void announce(uint32_t s) const {
+    st_shared4(s + 16, start, len, ref, h);
+    st_shared4(s + 32, tile, dq, nt, part);
+    st_shared4(s + 48, A, B0, lo, pad);
+    st_shared4(s, number, T, U, kq);
   }
   // Gives the slot back (one arrival per warp).
-  __device__ __forceinline__ void done(uint32_t bar0, int lane) {
+  static __device__ __forceinline__ void done(uint32_t bar0, int k, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar0 + 8u * (kBarItemFree + (k & 1)));
-    ++k;
   }
 };
 
 // The softmax warps of an item: P and dS of every tile of its sequence, then
 // the finished gradient tile from TMEM to memory.
-template <int D, bool DQ, typename P>
-__device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const P& p, int item_k, bool& ok) {
+template <int D, bool DQ>
+__device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const BwdTcParams& p, int item_k, bool& ok) {
   using C = Cfg<D>;
   constexpr int nA = C::kA, nB = C::kB;
-  Item item;
-  item.k = item_k;
-  item.read(bar0, p);
-  const BwdWork& w = item.w;
-  const BwdTiles& seq = item.seq;
+  Item w;
+  w.read(Item::slot(bar0, item_k));
   // Opaque, so that what follows from it is worked out per item, not kept in
   // registers over all of them for both kinds.
   int tid = threadIdx.x;
@@ -382,8 +376,8 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     const int row = quarter * 32 + lane, word0 = g * kWords, which = word0 / (D / 2);
     const uint32_t tile = bar0 - C::kSmBar + C::kSmRes + which * C::kTileBytes;
     const uint32_t dst = tmem + ((uint32_t)(quarter * 32) << 16) + kColA + word0;
-    if (item.k > 0) wait(kBarAccFree, item.k - 1);  // (over the last item's dV)
-    wait(kBarRes + which, item.k);
+    if (item_k > 0) wait(kBarAccFree, item_k - 1);  // (over the last item's dV)
+    wait(kBarRes + which, item_k);
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < kWords; k += 16) {
@@ -410,7 +404,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
   if (DQ) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)item.h * p.b.stat_stride + w.start + own0 + 8 * i]
+      const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)w.h * p.b.stat_stride + w.start + own0 + 8 * i]
                                              : make_float2(0.f, 0.f);
       nlse[i] = st.x;
       ndelta[i] = st.y;
@@ -423,7 +417,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     full0 = 0;
     full1 = (bidir || q0 >= w.ref ? w.ref : min(w.ref, q0 + 1)) / kTile;
   } else {   // no query before the last key, past the document, or past the first key's window
-    const int k0 = w.tile * kTile, first = seq.at(0) * kTile;
+    const int k0 = w.tile * kTile, first = w.B0 * kTile;
     const bool all_ref = k0 + kTile <= w.ref;
     const int from = all_ref && bidir ? 0 : k0 + kTile - 1;
     const long long to = all_ref ? w.len : min((long long)w.len, (long long)k0 + p.b.n);
@@ -431,13 +425,13 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     full1 = (int)((to - first) / kTile);
   }
   // (what only a masked tile needs is read back from the item's slot)
-  const int nt = item.nt, T = item.T, U = item.U, f0 = full0 - w.lo, f1 = full1 - w.lo;
-  const BwdTiles tiles = {seq.A - w.lo, seq.B0 + (DQ ? 0 : w.lo), w.lo};
+  const int nt = w.nt, T = w.T, U = w.U, f0 = full0 - w.lo, f1 = full1 - w.lo;
+  const int lo = w.lo, A = w.A - w.lo, B0 = w.B0 + (DQ ? 0 : w.lo);
 #pragma unroll 1
   for (int j = 0; j < nt; ++j) {
     const int odd = j & 1, it = T + j, iu = U + j;
     // first local row of the streamed tile
-    const int o0 = (DQ ? (j < tiles.A ? j + tiles.nB : tiles.B0 + j - tiles.A) : tiles.B0 + j) * kTile;
+    const int o0 = (DQ ? (j < A ? j + lo : B0 + j - A) : B0 + j) * kTile;
     const uint32_t tS = base + (DQ ? 0 : odd * 128);
     const uint32_t tP = base + (DQ ? 128 : (odd ^ 1) * 128);
     const bool full = j >= f0 && j < f1;
@@ -482,7 +476,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     }
     bool past_end = false;
     if (!full) {
-      const int len = ld_shared(slot + 16), ref = ld_shared(slot + 20);
+      const int len = ld_shared(slot + 20), ref = ld_shared(slot + 24);
       mask(x, len, ref);
       past_end = o0 + kTile > len;
       if (past_end) {  // rows of the streamed tiles past the document's end
@@ -546,9 +540,8 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
   // The item again from its slot: nothing of it but the loop's own stays in
   // registers over the loop.
   Item out;
-  out.k = item_k;
-  out.read(bar0, p);
-  const int own = out.w.tile * kTile + quarter * 32 + fg;
+  out.read(Item::slot(bar0, item_k));
+  const int own = out.tile * kTile + quarter * 32 + fg;
   // Blocks of 32 columns, a group each in turn: those of dQ, or of dV, then dK.
   constexpr int kBlocks = D / 32;
   const int H = p.b.H;
@@ -558,10 +551,10 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     float o[32];
     tmem_ld_frag(tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col, o);
     tmem_wait_ld();
-    if (out.w.part < 0) {
+    if (out.part < 0) {
       const float mul = !good ? __int_as_float(0x7fc00000) : !DQ && which == 0 ? 1.f : p.b.scale;
       __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
-                            ((size_t)(out.w.start + own) * H + out.h) * D + col + 8 * ft;
+                            ((size_t)(out.start + own) * H + out.h) * D + col + 8 * ft;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float* v = o + 16 * (i >> 1) + 2 * (i & 1);
@@ -571,11 +564,11 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
         // Words to the lane that holds their 16 bytes: a warp then writes 64
         // bytes of 8 rows at a time (a row per lane costs a pass per line).
         quad_transpose(q, ft);
-        if (own + 8 * i < out.w.len)
+        if (own + 8 * i < out.len)
           *reinterpret_cast<uint4*>(grad + (size_t)(8 * i) * H * D) = make_uint4(q[0], q[1], q[2], q[3]);
       }
     } else {
-      float* part = p.b.partials + (((size_t)out.w.part * H + out.h) * 2 + which) * kTile * D +
+      float* part = p.b.partials + (((size_t)out.part * H + out.h) * 2 + which) * kTile * D +
                     (quarter * 32 + fg) * D + col + 2 * ft;
       const float mul = good ? 1.f : __int_as_float(0x7fc00000);
 #pragma unroll
@@ -607,10 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int nA = C::kA, nB = C::kB;
 
   launch_dependents();
-  {  // the first item's entry, into the constant cache while the CTA sets up
-    const BwdWork& first = p.work[blockIdx.x / p.b.H];
-    asm volatile("" ::"r"(first.kind), "r"(first.start));
-  }
   if (threadIdx.x == 0) {
     constexpr int kWarps = kSoftmaxThreads / 32;
     for (int s = 0; s < kBarEnd + 1; ++s) {
@@ -633,43 +622,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
   const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
-  Item item;
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     if (lane == 0) {
       auto wait = [&](int slot, int phase) { return wait_phase(bar0, slot, phase); };
+      Item item;
       auto load = [&](uint32_t dst, const CUtensorMap* map, int tile, uint32_t bar) {
         mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
         for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, item.h, item.w.start + tile * kTile, bar);
+          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, item.h, item.start + tile * kTile, bar);
       };
       int a = 0, b = 0, r = 0;   // tiles issued on each ring, items whose own tiles were
-      int T = 0, U = 0, kq = 0;  // as Item's
+      item.T = item.U = item.kq = 0;
+      item.number = blockIdx.x;
       bool ok = true;
-      for (int id = blockIdx.x; ok;) {
-        const int k = item.k;
+      for (int k = 0; ok; ++k) {
         ok = wait(kBarItemFree + (k & 1), (k >> 1) + 1);
         if (!ok) break;
-        if (id >= p.n_items) id = -1;
-        const uint32_t slot = Item::slot(bar0, k);
-        st_shared(slot, id);
-        if (id >= 0) {
-          item.decode(p, id);
-          st_shared(slot + 4, T);
-          st_shared(slot + 8, U);
-          st_shared(slot + 12, kq);
-          st_shared(slot + 16, item.w.len);
-          st_shared(slot + 20, item.w.ref);
+        if (item.number >= p.n_items) {
+          item.number = -1;
+        } else {
+          const BwdWork& w = p.work[item.number / p.b.H];
+          item.h = item.number % p.b.H;
+          item.start = w.start;
+          item.len = w.len;
+          item.ref = w.ref;
+          item.tile = w.tile;
+          item.dq = w.kind == kBwdDQ;
+          item.nt = w.hi - w.lo;
+          item.part = w.part;
+          const BwdTiles seq = item.dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0)
+                                       : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0);
+          item.A = seq.A;
+          item.B0 = seq.B0;
+          item.lo = w.lo;
+          item.pad = 0;
         }
+        item.announce(Item::slot(bar0, k));
         mbar_arrive(B(kBarItem + (k & 1)));
-        if (id < 0) break;
+        if (item.number < 0) break;
         const bool dq = item.dq;
         const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
         const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
         for (int j = 0; j < item.nt; ++j) {
-          const int tile = item.seq.at(item.w.lo + j);
+          const int tile = item.at(j);
           ok = wait(kBarAFree + a % nA, a / nA + 1);
           if (!ok) break;
           load(smA + (a % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + a % nA));
@@ -677,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == 0) {
             ok = k == 0 || wait(kBarResFree, k - 1);
             if (!ok) break;
-            load(smRes, dq ? &p.tmQ : &p.tmK, item.w.tile, B(kBarRes));
-            load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, item.w.tile, B(kBarRes + 1));
+            load(smRes, dq ? &p.tmQ : &p.tmK, item.tile, B(kBarRes));
+            load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, item.tile, B(kBarRes + 1));
             ++r;
           }
           ok = wait(kBarBFree + b % nB, b / nB + 1);
@@ -686,13 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           load(smB + (b % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + b % nB));
           ++b;
         }
-        T += item.nt;
-        if (dq) ++kq;
-        else U += item.nt;
-        ++item.k;
+        item.T += item.nt;
+        if (dq) ++item.kq;
+        else item.U += item.nt;
         // The counter is zeroed by the kernel before this one.
         dependency_wait();
-        id = (int)gridDim.x + atomicAdd(p.b.counter, 1);
+        item.number = (int)gridDim.x + atomicAdd(p.b.counter, 1);
       }
       if (!ok) *s_abort = 1;
       // drain: every issued copy has landed before the CTA may exit
@@ -711,8 +708,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, wait_phase(bar0, slot, phase)) != 0;
     };
     bool ok = true;
-    while (ok && item.next(bar0, p)) {
-      const int nt = item.nt, T = item.T, U = item.U, k = item.k;
+    Item item;
+    for (int k = 0; ok && item.next(bar0, k); ++k) {
+      const int nt = item.nt, T = item.T, U = item.U;
       // stages of ring A: of the next S and of the next gradient product; of ring B: of the next dP
       int sa = T % nA, pa = T / nA & 1, ga = sa, sb = T % nB, pb = T / nB & 1, gb = sb;
       auto step = [](int& s, int n) { s = s + 1 == n ? 0 : s + 1; };
@@ -792,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       commit(lead, B(kBarFinal));
-      item.done(bar0, lane);
+      Item::done(bar0, k, lane);
     }
     if (!ok) *s_abort = 1;
     // every MMA issued by this thread has completed before TMEM is freed
@@ -802,36 +800,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- row statistics
     dependency_wait();
     bool ok = true;
-    while (ok && item.next(bar0, p)) {
+    Item item;
+    for (int k = 0; ok && item.next(bar0, k); ++k) {
       for (int j = 0; !item.dq && j < item.nt; ++j) {
         const int u = item.U + j, s = u & 1;
         ok = __all_sync(0xffffffffu, wait_phase(bar0, kBarStatsFree + s, (u >> 1) + 1));
         if (!ok) break;
         // (rows past the document's end are another's: zeros in their place)
-        const int q0 = item.seq.at(item.w.lo + j) * kTile;
-        const float2* src = p.b.stats + (size_t)item.h * p.b.stat_stride + item.w.start + q0;
+        const int q0 = item.at(j) * kTile;
+        const float2* src = p.b.stats + (size_t)item.h * p.b.stat_stride + item.start + q0;
         float* dst = reinterpret_cast<float*>(smem + C::kSmStats) + s * 2 * kTile;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 v = q0 + lane + 32 * i < item.w.len ? src[lane + 32 * i] : make_float2(0.f, 0.f);
+          const float2 v = q0 + lane + 32 * i < item.len ? src[lane + 32 * i] : make_float2(0.f, 0.f);
           dst[lane + 32 * i] = v.x;
           dst[kTile + lane + 32 * i] = v.y;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(B(kBarStats + s));
       }
-      item.done(bar0, lane);
+      Item::done(bar0, k, lane);
     }
   } else if (warp >= kSoftmaxWarp) {
     bool ok = true;
     for (int k = 0;; ++k) {
-      if (!Item::announced(bar0, k)) break;
-      const int id = k == 0 ? (int)blockIdx.x : ld_shared(Item::slot(bar0, k));
-      if (id < 0) break;
-      if (p.work[id / p.b.H].kind == kBwdDQ) softmax_item<D, true>(bar0, tmem, p, k, ok);
+      if (!__all_sync(0xffffffffu, wait_phase(bar0, kBarItem + (k & 1), k >> 1))) break;
+      const uint32_t slot = Item::slot(bar0, k);
+      if (ld_shared(slot) < 0) break;
+      if (ld_shared(slot + 36)) softmax_item<D, true>(bar0, tmem, p, k, ok);
       else softmax_item<D, false>(bar0, tmem, p, k, ok);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(B(kBarItemFree + (k & 1)));
+      Item::done(bar0, k, lane);
     }
   }
   tc_fence_before();
