@@ -109,10 +109,11 @@ enum : int {
   kBarDP = 31,
   kBarRead = 32,      // dK, dV items: dP is read; dQ items: S is
   kBarFinal = 33,     // the item's last MMA is done
-  kBarStats = 34,     // 2 (dK, dV items)
-  kBarStatsFree = 36, // 2
-  kBarEnd = 38,
-  kSlotTmem = 39, kSlotAbort = 40, kSlotItem = 42  // 2 x 64 bytes: Item::Slot
+  kBarFinalV = 34,    // dK, dV items: the last into dV is
+  kBarStats = 35,     // 2 (dK, dV items)
+  kBarStatsFree = 37, // 2
+  kBarEnd = 39,
+  kSlotTmem = 40, kSlotAbort = 41, kSlotItem = 42  // 2 x 64 bytes: Item::Slot
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -533,26 +534,31 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     }
   }
   // -------------------------------------------------- the tile's gradient
-  wait(kBarFinal, item_k);
-  tc_fence_after();
-  if (!ok) st_shared(bar0 + 8u * kSlotAbort, 1);
-  const bool good = ok && !ld_shared(bar0 + 8u * kSlotAbort);
   // The item again from its slot: nothing of it but the loop's own stays in
   // registers over the loop.
   Item out;
   out.read(Item::slot(bar0, item_k));
   const int own = out.tile * kTile + quarter * 32 + fg;
-  // Blocks of 32 columns, a group each in turn: those of dQ, or of dV, then dK.
+  // Blocks of 32 columns, a group each in turn: those of dQ, or of dV (complete
+  // before the last dS is), then dK.
   constexpr int kBlocks = D / 32;
   const int H = p.b.H;
 #pragma unroll 1
-  for (int blk = g; blk < (DQ ? 1 : 2) * kBlocks; blk += kSoftmaxThreads / 128) {
+  for (int blk = g; blk < (DQ ? 1 : 2) * kBlocks; blk += 4) {
     const int which = blk / kBlocks, col = blk % kBlocks * 32;
+    if (!DQ && which == 0) wait(kBarFinalV, item_k - out.kq);
+    else wait(kBarFinal, item_k);
+    tc_fence_after();
     float o[32];
     tmem_ld_frag(tmem + ((uint32_t)(quarter * 32) << 16) + (DQ ? 384 : 256 + 128 * which) + col, o);
     tmem_wait_ld();
+    const bool good = ok && !ld_shared(bar0 + 8u * kSlotAbort);
+    if (DQ || which == 1 || !good) {
+      const float mul = !good ? __int_as_float(0x7fc00000) : out.part < 0 ? p.b.scale : 1.f;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] *= mul;
+    }
     if (out.part < 0) {
-      const float mul = !good ? __int_as_float(0x7fc00000) : !DQ && which == 0 ? 1.f : p.b.scale;
       __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(DQ ? p.b.dQ : which == 0 ? p.b.dV : p.b.dK) +
                             ((size_t)(out.start + own) * H + out.h) * D + col + 8 * ft;
 #pragma unroll
@@ -560,7 +566,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
         const float* v = o + 16 * (i >> 1) + 2 * (i & 1);
         uint32_t q[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = pack_bf16x2(v[4 * k] * mul, v[4 * k + 1] * mul);
+        for (int k = 0; k < 4; ++k) q[k] = pack_bf16x2(v[4 * k], v[4 * k + 1]);
         // Words to the lane that holds their 16 bytes: a warp then writes 64
         // bytes of 8 rows at a time (a row per lane costs a pass per line).
         quad_transpose(q, ft);
@@ -570,16 +576,16 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     } else {
       float* part = p.b.partials + (((size_t)out.part * H + out.h) * 2 + which) * kTile * D +
                     (quarter * 32 + fg) * D + col + 2 * ft;
-      const float mul = good ? 1.f : __int_as_float(0x7fc00000);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float* v = o + 16 * (i >> 1) + 2 * (i & 1) + 4 * k;
-          *reinterpret_cast<float2*>(part + 8 * i * D + 8 * k) = make_float2(v[0] * mul, v[1] * mul);
+          *reinterpret_cast<float2*>(part + 8 * i * D + 8 * k) = make_float2(v[0], v[1]);
         }
     }
   }
+  if (!ok) st_shared(bar0 + 8u * kSlotAbort, 1);
   tc_fence_before();
   arrive(kBarAccFree);
 }
@@ -778,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           mma_grad<D>(lead, dV, tmem + (j & 1) * 128, smB + gb * C::kTileBytes, j > 0);
           commit(lead, B(kBarBFree + gb));
+          if (j == nt - 1) commit(lead, B(kBarFinalV));
           step(gb, nB);
           if (j + 1 < nt) ok = wait(kBarRead, T + j) && scores(j + 1);
           ok = ok && wait(kBarDS + ((T + j) & 1), (T + j) >> 1);
