@@ -21,7 +21,6 @@ inside RSWA.append_decode, RSWA.prefill and masked_attention (rotary=...).
 from __future__ import annotations
 
 import ctypes as C
-import functools
 from typing import Optional, Sequence
 
 import numpy as np
@@ -394,20 +393,7 @@ def _pack_args(Q: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[in
     n_docs = len(ref_lens)
     if len(cu_seqlens) != n_docs + 1 or int(cu_seqlens[-1]) != L:
         raise ValueError("cu_seqlens must have len(ref_lens) + 1 entries ending at L")
-    return (L, H, d) + _documents(tuple(map(int, cu_seqlens)), tuple(map(int, ref_lens)))
-
-
-@functools.lru_cache(maxsize=64)
-def _documents(cu_seqlens: tuple, ref_lens: tuple) -> tuple:
-    """The documents as host arrays for the library, which only reads them."""
-    return (C.c_int32 * len(cu_seqlens))(*cu_seqlens), (C.c_int32 * max(len(ref_lens), 1))(*ref_lens)
-
-
-@functools.lru_cache(maxsize=64)
-def _backward_workspace_bytes(cu_seqlens: tuple, ref_lens: tuple, n: int, H: int, d: int, dtype: int, flags: int) -> int:
-    """A pure function of the sizes, that plans the whole call: remembered."""
-    return _native.lib().rswa_masked_backward_workspace_bytes(*_documents(cu_seqlens, ref_lens), len(ref_lens), n, H, d,
-                                                              dtype, flags)
+    return L, H, d, (C.c_int32 * (n_docs + 1))(*map(int, cu_seqlens)), (C.c_int32 * max(n_docs, 1))(*map(int, ref_lens))
 
 
 def _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, out, bidir_prefix):
@@ -500,6 +486,14 @@ def masked_backward_varlen(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V
                            lse: torch.Tensor, cu_seqlens: Sequence[int], ref_lens: Sequence[int], n: int,
                            scale: float = 0.0, out=None, bidir_prefix: bool = False) -> tuple:
     """Gradient of masked_forward_varlen, as masked_backward: (dQ, dK, dV)."""
+    if out is None:
+        r = _native.binding().backward(dO, Q, K, V, O, lse, cu_seqlens, ref_lens, n, scale,
+                                       _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0)
+        if r.__class__ is tuple:
+            return r
+        if r is not None:
+            check(r)
+    # Given results, argument types the short way leaves alone, or something that does not fit.
     L, H, d, cu, refs = _pack_args(Q, cu_seqlens, ref_lens)
     shape, index = Q.shape, Q.get_device()
     if out is None:
@@ -518,7 +512,7 @@ def masked_backward_varlen(dO: torch.Tensor, Q: torch.Tensor, K: torch.Tensor, V
     lib = _native.lib()
     dt, docs, n = _DT[Q.dtype], len(ref_lens), int(n)
     flags = _native.FLAG_BIDIR_PREFIX if bidir_prefix else 0
-    ws_bytes = _backward_workspace_bytes(tuple(map(int, cu_seqlens)), tuple(map(int, ref_lens)), n, H, d, dt, flags)
+    ws_bytes = lib.rswa_masked_backward_workspace_bytes(cu, refs, docs, n, H, d, dt, flags)
     # 0 bytes: arguments that the call itself reports
     ws = Q.new_empty((max(ws_bytes, 16),), dtype=torch.uint8)
     _call(index, lib.rswa_masked_backward, dO.data_ptr(), Q.data_ptr(), K.data_ptr(), V.data_ptr(), O.data_ptr(),
@@ -551,7 +545,18 @@ class Rotary:
                                              float(base), self._SCALINGS[scaling], float(factor),
                                              int(original_length)))
         self.mscale = self._plan.mscale
-        self._ref, self._apply = C.byref(self._plan), _native.lib().rswa_rotary_apply
+        self._ref, self._address = C.byref(self._plan), C.addressof(self._plan)
+        self._rotary = _native.binding().rotary
+        self._made_from = (d, rotary_dim, base, interleaved, scaling, factor, original_length)
+
+    def __reduce__(self):  # copies and pickles are made anew: the plan's address is this object's own
+        return Rotary, self._made_from
+
+    def __call__(self, Q: torch.Tensor, K: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 first: int = 0):
+        """apply as a differentiable function of Q and K."""
+        r = _Turn.apply(self, positions, first, *((Q,) if K is None else (Q, K)))
+        return r[0] if K is None else r
 
     def _stride(self, name: str, t: torch.Tensor, rows: int, like: torch.Tensor, index: int) -> int:
         """Checks t ([rows, heads, d] with contiguous heads, a slice of wider
@@ -570,59 +575,51 @@ class Rotary:
 
     def apply(self, Q: torch.Tensor, K: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
               first: int = 0, inverse: bool = False, out=None):
-        """Q (and K) [rows, heads, d] turned to their positions, in one launch.
+        """Q (and K) [rows, heads, d] turned to their positions, in one launch
+        (calling the plan itself is the differentiable form).
 
         positions: int32 [rows] on the device; None: first, first + 1, ...
         inverse: turned back by the same angles (the gradient).
         Rows may be slices of wider ones (a fused projection); out (Q's
         result, or the pair) may be such slices too, or the inputs
         themselves.  Returns Q's result, or the pair."""
+        if out is None:
+            r = self._rotary(self._address, Q, K, positions, first, inverse)
+            if r.__class__ is int:
+                check(r)
+            if r is not None:
+                return r
+        # Given results, a subclass of Tensor, or something that does not fit.
         if not isinstance(Q, torch.Tensor):
             raise TypeError("Q must be a torch.Tensor")
-        if K is not None and not isinstance(K, torch.Tensor):
-            raise TypeError("K must be a torch.Tensor")
         if not Q.is_cuda:
             raise ValueError(f"Q is on {Q.device}, expected a CUDA device")
-        dt = _DT.get(Q.dtype)
-        if dt is None:
+        if Q.dtype not in _DT:
             raise ValueError(f"dtype {Q.dtype} not supported")
-        shape = Q.shape
-        rows = shape[0] if len(shape) == 3 else 0
+        rows, index = (Q.shape[0] if Q.dim() == 3 else 0), Q.get_device()
+        ins = (Q,) if K is None else (Q, K)
+        strides = [self._stride(name, t, rows, Q, index) for name, t in zip(("Q", "K"), ins)]
         if out is None:
-            # (empty_like of a contiguous tensor is, and is the cheaper call)
-            q = torch.empty_like(Q) if Q.is_contiguous() else torch.empty_like(Q, memory_format=torch.contiguous_format)
-            k = (None if K is None else torch.empty_like(K) if K.is_contiguous()
-                 else torch.empty_like(K, memory_format=torch.contiguous_format))
+            outs = tuple(torch.empty_like(t, memory_format=torch.contiguous_format) for t in ins)
         else:
-            q, k = (out, None) if K is None else out
-        index, d = Q.get_device(), self.d
+            outs = (out,) if K is None else tuple(out)
+        if len(outs) != len(ins):
+            raise ValueError("out must hold one tensor for Q and one for K")
+        args = []
+        for name, t, s, o in zip(("Q", "K"), ins, strides, outs):
+            so = self._stride("out of " + name, o, rows, Q, index)
+            if o.shape != t.shape:
+                raise ValueError(f"out of {name} has shape {tuple(o.shape)}, expected {tuple(t.shape)}")
+            args += [t.data_ptr(), s, t.shape[1], o.data_ptr(), so]
+        if K is None:
+            args += [None, 0, 0, None, 0]
         pos = None
         if positions is not None:
-            if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.dim() == 1
-                    and positions.shape[0] == rows and positions.get_device() == index and positions.is_contiguous()):
-                _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
+            _check_tensor("positions", positions, (rows,), torch.int32, Q.device)
             pos = positions.data_ptr()
-        sq = self._stride("Q", Q, rows, Q, index)
-        if out is None:
-            sqo = shape[1] * d
-        else:
-            sqo = self._stride("out of Q", q, rows, Q, index)
-            if q.shape != shape:
-                raise ValueError(f"out of Q has shape {tuple(q.shape)}, expected {tuple(shape)}")
-        if K is None:
-            keys = (None, 0, 0, None, 0)
-        else:
-            sk, heads = self._stride("K", K, rows, Q, index), K.shape[1]
-            if out is None:
-                sko = heads * d
-            else:
-                sko = self._stride("out of K", k, rows, Q, index)
-                if k.shape != K.shape:
-                    raise ValueError(f"out of K has shape {tuple(k.shape)}, expected {tuple(K.shape)}")
-            keys = (K.data_ptr(), sk, heads, k.data_ptr(), sko)
-        _call(index, self._apply, self._ref, Q.data_ptr(), sq, shape[1], q.data_ptr(), sqo, *keys, pos, int(first), rows,
-              dt, 1 if inverse else 0, _stream_ptr(Q.device))
-        return q if K is None else (q, k)
+        _call(index, _native.lib().rswa_rotary_apply, self._ref, *args, pos, int(first), rows, _DT[Q.dtype],
+              1 if inverse else 0, _stream_ptr(Q.device))
+        return outs[0] if K is None else outs
 
 
 def document_positions(cu_seqlens: Sequence[int], device=None) -> torch.Tensor:
@@ -633,6 +630,23 @@ def document_positions(cu_seqlens: Sequence[int], device=None) -> torch.Tensor:
         raise ValueError("cu_seqlens must start at 0 and increase")
     pos = np.arange(cu[-1], dtype=np.int64) - np.repeat(cu[:-1], np.diff(cu))
     return torch.from_numpy(pos.astype(np.int32)).to(torch.device("cuda") if device is None else device)
+
+
+class _Turn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, rotary, positions, first, Q, K=None):
+        ctx.rotary, ctx.first = rotary, first
+        ctx.save_for_backward(positions)
+        r = rotary.apply(Q, K, positions=positions, first=first)
+        return (r,) if K is None else r
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dQ, dK=None):
+        positions, = ctx.saved_tensors
+        g = (dQ.contiguous(),) if dK is None else (dQ.contiguous(), dK.contiguous())
+        r = ctx.rotary.apply(*g, positions=positions, first=ctx.first, inverse=True)
+        return (None, None, None) + ((r,) if dK is None else r)
 
 
 class _MaskedAttention(torch.autograd.Function):

@@ -73,6 +73,25 @@ _PROTOS = {
 _lib = None
 
 
+_binding = None
+
+
+def binding():
+    """The compiled binding (binding/binding.cpp), bound to the same library on first use."""
+    global _binding
+    if _binding is None:
+        handle = lib()
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError(f"reference_sliding_window_b200/_binding.so is missing or does not load ({e}): build it with "
+                              "`python -m reference_sliding_window_b200.build`") from e
+        module.bind(*(C.cast(getattr(handle, f), _p).value for f in (
+            "rswa_masked_backward", "rswa_masked_backward_workspace_bytes", "rswa_rotary_apply")))
+        _binding = module
+    return _binding
+
+
 class RSWAError(RuntimeError):
     def __init__(self, status: int, message: str):
         name = STATUS_NAMES[status] if 0 <= status < len(STATUS_NAMES) else str(status)

@@ -5,6 +5,8 @@
 Each csrc/*.cu is compiled to an object in parallel, then linked into
 reference_sliding_window_b200/librswa.so.  The CUDA runtime is linked
 statically (nvcc's default), so the library only needs the driver.
+binding/binding.cpp (the short way in from Python) is compiled by the host
+compiler against torch into reference_sliding_window_b200/_binding.so.
 """
 
 from __future__ import annotations
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,6 +25,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "librswa.so")
+BINDING_SRC = os.path.join(PKG, "binding", "binding.cpp")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -54,6 +59,27 @@ def _compile(src: str, obj: str, extra) -> None:
         sys.stderr.write(r.stderr)
 
 
+def build_binding(force: bool = False) -> None:
+    deps = (BINDING_SRC, os.path.join(INCLUDE, "rswa.h"))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = BINDING + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), BINDING_SRC,
+           "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"binding.cpp failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -65,8 +91,8 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if force or not os.path.exists(o) or os.path.getmtime(o) < max(os.path.getmtime(s), hdr_t):
             todo.append((s, o))
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=min(8, max(1, len(todo)))) as ex:
-        for f in [ex.submit(_compile, s, o, extra) for s, o in todo]:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(todo) + 1)) as ex:
+        for f in [ex.submit(build_binding, force)] + [ex.submit(_compile, s, o, extra) for s, o in todo]:
             f.result()
     if todo or not os.path.exists(LIB):
         tmp = LIB + ".tmp"

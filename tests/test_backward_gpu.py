@@ -308,6 +308,18 @@ def test_decode_after_a_turned_prefill():
     a.check()
 
 
+def test_both_ways_into_the_library_agree():
+    """Given results, and documents as an array, take the longer way in."""
+    cu, refs, n = [0, 200, 333], [90, 40], 25
+    dO, Q, K, V = _inputs(cu[-1], 2, 64, "bf16", seed=60)
+    O, lse = masked_forward_varlen(Q, K, V, cu, refs, n, return_lse=True)
+    a = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n)
+    b = masked_backward_varlen(dO, Q, K, V, O, lse, np.array(cu), np.array(refs), np.int64(n))
+    c = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n, out=[torch.empty_like(Q) for _ in range(3)])
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, y) and torch.equal(x, z)
+
+
 def test_refusals():
     dO, Q, K, V = _inputs(16, 2, 64, "f32", seed=1)
     O, lse = masked_forward(Q, K, V, L_m=4, n=2, return_lse=True)

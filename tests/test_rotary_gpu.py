@@ -2,6 +2,8 @@
 
 from __future__ import annotations
 
+import copy
+
 import pytest
 import torch
 
@@ -120,6 +122,38 @@ def test_gradient_is_the_inverse_turn():
         f = [(gradients.rotate(x.double() + s * 1e-3 * v, torch.arange(9), th, m) * gy.double()).sum() for s in (1, -1)]
         diff = ((f[0] - f[1]) / 2e-3).item()  # linear: exact up to rounding
         assert abs((gx * v).sum().item() - diff) <= 2.0 ** -20 * (gy.double().norm() * v.norm() * m).item()
+
+
+@pytest.mark.parametrize("pair", [False, True])
+def test_differentiable_call_and_copies(pair):
+    rot = copy.deepcopy(Rotary(64, rotary_dim=40, interleaved=True, scaling="linear", factor=3.0))
+    th, m = gradients.thetas(40, scaling="linear", factor=3.0)
+    x = [torch.randn(7, h, 64, device="cuda", requires_grad=True) for h in ((3, 2) if pair else (3,))]
+    pos = torch.arange(7, dtype=torch.int32, device="cuda") * 11
+    y = rot(*x, positions=pos)
+    y = y if pair else (y,)
+    g = [torch.randn_like(t).transpose(0, 1).contiguous().transpose(0, 1) for t in y]  # not contiguous
+    torch.autograd.backward(y, g)
+    for t, o, go in zip(x, y, g):
+        _close(o.detach(), t.detach(), pos, dict(rotary_dim=40, interleaved=True, scaling="linear", factor=3.0))
+        want = gradients.rotate(go.cpu(), pos.cpu(), th, m, True, True)
+        assert ((t.grad.double().cpu() - want).abs() <= gradients.rotary_bound(go.cpu(), want, m)).all()
+    with pytest.raises(ValueError):
+        rot(torch.zeros(3, 2, 32, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_both_ways_into_the_library_agree(dtype):
+    """A tensor subclass and given results take the longer way in."""
+    class Sub(torch.Tensor):
+        pass
+    Q, K = (synth.normal((9, h, 64), h, dtype).cuda() for h in (3, 1))
+    rot = Rotary(64)
+    a = rot.apply(Q, K, first=5)
+    b = rot.apply(Q.as_subclass(Sub), K, first=5)
+    c = rot.apply(Q, K, first=5, out=(torch.empty_like(Q), torch.empty_like(K)))
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, torch.as_tensor(y)) and torch.equal(x, z)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
