@@ -80,7 +80,10 @@ size_t stats_bytes(int L, int H) { return align_up(sizeof(float2) * (size_t)H * 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParams p) {
   constexpr int N = Vec16<T>::N, G = D / N;
-  launch_dependents();  // the items load their tiles while the statistics form
+  dependency_wait();
+  // The items may load their tiles while the statistics form: whatever wrote
+  // their tensors is done.
+  launch_dependents();
   const long long idx = (long long)blockIdx.x * 256 + threadIdx.x;
   if (idx < p.n_counters) p.counter[idx] = 0;
   const long long rh = idx / G;  // row * H + head
@@ -105,8 +108,7 @@ __global__ void __launch_bounds__(256) backward_stats_kernel(const BackwardParam
 template <typename T, int D>
 cudaError_t launch_stats(const BackwardParams& p, cudaStream_t stream) {
   const long long threads = (long long)p.L * p.H * (D / Vec16<T>::N);
-  backward_stats_kernel<T, D><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(backward_stats_kernel<T, D>, (unsigned)((threads + 255) / 256), 256, 0, stream, p);
 }
 
 constexpr int kMaxJoin = 1000;

@@ -606,6 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int nA = C::kA, nB = C::kB;
 
   launch_dependents();
+  if (threadIdx.x < 4) {
+    const CUtensorMap* map = threadIdx.x == 0 ? &p.tmQ : threadIdx.x == 1 ? &p.tmK : threadIdx.x == 2 ? &p.tmV : &p.tmG;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+  }
   if (threadIdx.x == 0) {
     constexpr int kWarps = kSoftmaxThreads / 32;
     for (int s = 0; s < kBarEnd + 1; ++s) {
