@@ -621,6 +621,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     *s_abort = (sbase & 1023) != 0;
     fence_barrier_init();
   }
+  const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
+  // The producer's steps (thread 0).  The first item's first loads are issued
+  // before the CTA has set itself up: they need the barriers, which thread 0
+  // has just made, and nothing else.
+  Item item;
+  int a = 0, b = 0;  // tiles issued on each ring
+  auto load = [&](uint32_t dst, const CUtensorMap* map, int tile, uint32_t bar) {
+    mbar_arrive_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+    for (int x = 0; x < C::kBoxes; ++x)
+      tma_load_3d(dst + x * kBoxBytes, map, kBox * x, item.h, item.start + tile * kTile, bar);
+  };
+  auto load_a = [&](int j) {
+    load(smA + (a % nA) * C::kTileBytes, item.dq ? &p.tmK : &p.tmQ, item.at(j), B(kBarAFull + a % nA));
+    ++a;
+  };
+  auto load_b = [&](int j) {
+    load(smB + (b % nB) * C::kTileBytes, item.dq ? &p.tmV : &p.tmG, item.at(j), B(kBarBFull + b % nB));
+    ++b;
+  };
+  auto load_res = [&] {
+    load(smRes, item.dq ? &p.tmQ : &p.tmK, item.tile, B(kBarRes));
+    load(smRes + C::kTileBytes, item.dq ? &p.tmG : &p.tmV, item.tile, B(kBarRes + 1));
+  };
+  auto announce = [&](int k) {  // item.number's description, or the end
+    if (item.number >= p.n_items) {
+      item.number = -1;
+    } else {
+      const BwdWork& w = p.work[item.number / p.b.H];
+      item.h = item.number % p.b.H;
+      item.start = w.start;
+      item.len = w.len;
+      item.ref = w.ref;
+      item.tile = w.tile;
+      item.dq = w.kind == kBwdDQ;
+      item.nt = w.hi - w.lo;
+      item.part = w.part;
+      const BwdTiles seq = item.dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0)
+                                   : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0);
+      item.A = seq.A;
+      item.B0 = seq.B0;
+      item.lo = w.lo;
+      item.pad = 0;
+    }
+    item.announce(Item::slot(bar0, k));
+    mbar_arrive(B(kBarItem + (k & 1)));
+  };
+  if (threadIdx.x == 0) {
+    item.T = item.U = item.kq = 0;
+    item.number = blockIdx.x;
+    announce(0);
+    load_a(0);
+    load_res();
+    load_b(0);
+  }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((const void*)s_tmem)),
                  "r"(kTmemCols)
@@ -631,71 +686,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer
     if (lane == 0) {
       auto wait = [&](int slot, int phase) { return wait_phase(bar0, slot, phase); };
-      Item item;
-      auto load = [&](uint32_t dst, const CUtensorMap* map, int tile, uint32_t bar) {
-        mbar_arrive_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-        for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_3d(dst + x * kBoxBytes, map, kBox * x, item.h, item.start + tile * kTile, bar);
-      };
-      int a = 0, b = 0, r = 0;   // tiles issued on each ring, items whose own tiles were
-      item.T = item.U = item.kq = 0;
-      item.number = blockIdx.x;
       bool ok = true;
+      int r = 1;  // items whose own tiles were issued
       for (int k = 0; ok; ++k) {
-        ok = wait(kBarItemFree + (k & 1), (k >> 1) + 1);
-        if (!ok) break;
-        if (item.number >= p.n_items) {
-          item.number = -1;
-        } else {
-          const BwdWork& w = p.work[item.number / p.b.H];
-          item.h = item.number % p.b.H;
-          item.start = w.start;
-          item.len = w.len;
-          item.ref = w.ref;
-          item.tile = w.tile;
-          item.dq = w.kind == kBwdDQ;
-          item.nt = w.hi - w.lo;
-          item.part = w.part;
-          const BwdTiles seq = item.dq ? bwd_key_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0)
-                                       : bwd_query_tiles(kTile, w.tile, w.len, w.ref, p.b.n, p.b.bidir != 0);
-          item.A = seq.A;
-          item.B0 = seq.B0;
-          item.lo = w.lo;
-          item.pad = 0;
+        if (k > 0) {
+          ok = wait(kBarItemFree + (k & 1), (k >> 1) + 1);
+          if (!ok) break;
+          announce(k);
+          if (item.number < 0) break;
         }
-        item.announce(Item::slot(bar0, k));
-        mbar_arrive(B(kBarItem + (k & 1)));
-        if (item.number < 0) break;
-        const bool dq = item.dq;
-        const CUtensorMap* mapA = dq ? &p.tmK : &p.tmQ;
-        const CUtensorMap* mapB = dq ? &p.tmV : &p.tmG;
-        for (int j = 0; j < item.nt; ++j) {
-          const int tile = item.at(j);
+        for (int j = k == 0 ? 1 : 0; j < item.nt; ++j) {
           ok = wait(kBarAFree + a % nA, a / nA + 1);
           if (!ok) break;
-          load(smA + (a % nA) * C::kTileBytes, mapA, tile, B(kBarAFull + a % nA));
-          ++a;
+          load_a(j);
           if (j == 0) {
-            ok = k == 0 || wait(kBarResFree, k - 1);
+            ok = wait(kBarResFree, k - 1);
             if (!ok) break;
-            load(smRes, dq ? &p.tmQ : &p.tmK, item.tile, B(kBarRes));
-            load(smRes + C::kTileBytes, dq ? &p.tmG : &p.tmV, item.tile, B(kBarRes + 1));
+            load_res();
             ++r;
           }
           ok = wait(kBarBFree + b % nB, b / nB + 1);
           if (!ok) break;
-          load(smB + (b % nB) * C::kTileBytes, mapB, tile, B(kBarBFull + b % nB));
-          ++b;
+          load_b(j);
         }
         item.T += item.nt;
-        if (dq) ++item.kq;
+        if (item.dq) ++item.kq;
         else item.U += item.nt;
         // The counter is zeroed by the kernel before this one.
         dependency_wait();
@@ -703,10 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) *s_abort = 1;
       // drain: every issued copy has landed before the CTA may exit
-      if (r > 0) {
-        mbar_wait_bounded(B(kBarRes), (r - 1) & 1);
-        mbar_wait_bounded(B(kBarRes + 1), (r - 1) & 1);
-      }
+      mbar_wait_bounded(B(kBarRes), (r - 1) & 1);
+      mbar_wait_bounded(B(kBarRes + 1), (r - 1) & 1);
       for (int j = max(0, a - nA); j < a; ++j) mbar_wait_bounded(B(kBarAFull + j % nA), (j / nA) & 1);
       for (int j = max(0, b - nB); j < b; ++j) mbar_wait_bounded(B(kBarBFull + j % nB), (j / nB) & 1);
     }
@@ -718,7 +736,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       return __all_sync(0xffffffffu, wait_phase(bar0, slot, phase)) != 0;
     };
     bool ok = true;
-    Item item;
     for (int k = 0; ok && item.next(bar0, k); ++k) {
       const int nt = item.nt, T = item.T, U = item.U;
       // stages of ring A: of the next S and of the next gradient product; of ring B: of the next dP
@@ -811,7 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------- row statistics
     dependency_wait();
     bool ok = true;
-    Item item;
     for (int k = 0; ok && item.next(bar0, k); ++k) {
       for (int j = 0; !item.dq && j < item.nt; ++j) {
         const int u = item.U + j, s = u & 1;
