@@ -306,8 +306,10 @@ rswa_status rswa_masked_forward_lse(const void* Q, const void* K, const void* V,
  *     its contents need no preparation and mean nothing afterwards.  Calls
  *     that may run at the same time need workspaces of their own.
  * Every gradient element is summed in one fixed order in float32: the same
- * call gives the same bits.  Every argument is checked before anything is
- * enqueued; the host arrays are read during the call only. */
+ * call gives the same bits.  An infinity or a NaN in one document leaves the
+ * others' gradients as they are.  Every argument is checked before anything is
+ * enqueued; the host arrays are read during the call only.  Should a kernel's
+ * bounded wait run out, the rows that it worked on are NaN. */
 size_t rswa_masked_backward_workspace_bytes(const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n,
                                             int H, int d, rswa_dtype dtype, int flags);
 rswa_status rswa_masked_backward(const void* dO, const void* Q, const void* K, const void* V, const void* O,
