@@ -295,7 +295,7 @@ def run_varlen(iters: int, warmup: int):
 
 
 DECODE_SOURCES = ("decode.cu", "common.cuh", "internal.h")
-PREFILL_SOURCES = ("masked_tc.cu", "common.cuh")  # the kernel takes its parameters from masked_tc.cu
+PREFILL_SOURCES = ("masked_tc.cu", "tc.cuh", "common.cuh")  # the kernel takes its parameters from masked_tc.cu
 
 
 def _code_only(text: str) -> str:

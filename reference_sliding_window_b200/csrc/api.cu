@@ -20,6 +20,7 @@
 #include "backward.h"
 #include "cache_copy.h"
 #include "internal.h"
+#include "masked_lse.h"
 #include "rotary.h"
 #include "rswa.h"
 
@@ -864,8 +865,6 @@ static rswa_status masked_forward_one(const void* Q, const void* K, const void* 
   const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
   p.scale_log2 = sc * 1.4426950408889634f;
   p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
-  p.lse = lse;
-  p.lse_stride = lse_stride;
   p.timing = g_timing;
   const int32_t cu[2] = {0, L}, refs[1] = {L_m};
   p.cu = cu;
@@ -875,9 +874,9 @@ static rswa_status masked_forward_one(const void* Q, const void* K, const void* 
   p.fill_S_cap = p.fill_n = p.fill_full = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dtype == RSWA_BF16 && d == 128) {
-    RSWA_CUDA(launch_masked_forward_tc(p, s), "masked forward tensor-core kernel");
+    RSWA_CUDA(launch_masked_forward_tc(p, RowLse{lse, lse_stride}, s), "masked forward tensor-core kernel");
   } else {
-    RSWA_CUDA(launch_masked_forward_simt(p, dtype == RSWA_BF16 ? kBF16 : kF32, s), "masked forward kernel");
+    RSWA_CUDA(launch_masked_forward_simt(p, dtype == RSWA_BF16 ? kBF16 : kF32, RowLse{lse, lse_stride}, s), "masked forward kernel");
   }
   return RSWA_OK;
 }
@@ -948,15 +947,13 @@ static rswa_status masked_forward_pack(const void* Q, const void* K, const void*
     const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)d);
     p.scale_log2 = sc * 1.4426950408889634f;
     p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
-    p.lse = lse;
-    p.lse_stride = cu_seqlens[n_docs];
     p.timing = g_timing;
     p.cu = cu_seqlens;
     p.refs = ref_lens;
     p.n_docs = n_docs;
     p.fill_kc = p.fill_vc = nullptr;
     p.fill_S_cap = p.fill_n = p.fill_full = 0;
-    RSWA_CUDA(launch_masked_forward_tc(p, static_cast<cudaStream_t>(stream)), "masked forward tensor-core kernel");
+    RSWA_CUDA(launch_masked_forward_tc(p, RowLse{lse, cu_seqlens[n_docs]}, static_cast<cudaStream_t>(stream)), "masked forward tensor-core kernel");
     return RSWA_OK;
   }
   // CUDA-core kernel: each document is a contiguous [len][H][d] slice of the pack.
@@ -1017,8 +1014,6 @@ extern "C" rswa_status rswa_masked_forward_fill(rswa_handle h, const void* Q, co
     const float sc = scale > 0.f ? scale : 1.0f / sqrtf((float)h->d);
     p.scale_log2 = sc * 1.4426950408889634f;
     p.bidir_prefix = (flags & RSWA_FLAG_BIDIR_PREFIX) ? 1 : 0;
-    p.lse = nullptr;
-    p.lse_stride = 0;
     p.timing = g_timing;
     const int32_t cu[2] = {0, L}, refs[1] = {L_m};
     p.cu = cu;

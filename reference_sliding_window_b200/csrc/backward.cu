@@ -6,7 +6,7 @@
 #include <algorithm>
 #include <vector>
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace rswa {
 namespace {

@@ -27,7 +27,7 @@
 #include <algorithm>
 
 #include "backward.h"
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace rswa {
 namespace {

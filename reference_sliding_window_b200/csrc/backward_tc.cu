@@ -48,7 +48,7 @@
 #include <algorithm>
 
 #include "backward.h"
-#include "common.cuh"
+#include "launch.cuh"
 #include "tc.cuh"
 
 namespace rswa {

@@ -199,10 +199,6 @@ struct MaskedParams {
   int L, L_m, n, H, D;
   float scale_log2;
   int bidir_prefix;             // 1: prefix queries see every reference key
-  // Natural log of each row's sum of exponentials, [H][lse_stride] float32
-  // (what the gradient recomputes the probabilities from), or null.
-  float* lse;
-  int lse_stride;
   unsigned long long* timing;  // profiling stamps (RSWA_TIMING builds), may be null
   // Documents of a pack (tensor-core kernel): document i holds rows
   // [cu[i], cu[i+1]) with refs[i] reference rows; HOST arrays.  The

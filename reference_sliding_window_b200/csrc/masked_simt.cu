@@ -11,7 +11,7 @@
 #include <math.h>
 
 #include "common.cuh"
-#include "internal.h"
+#include "masked_lse.h"
 
 namespace rswa {
 
@@ -19,7 +19,7 @@ constexpr int kSimtWarps = 4;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kSimtWarps * 32)
-masked_simt_kernel(const __grid_constant__ MaskedParams p) {
+masked_simt_kernel(const __grid_constant__ MaskedParams p, const RowLse out) {
   constexpr int DPL = D / 32;  // output elements per lane
   __shared__ float qs[kSimtWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -86,17 +86,21 @@ masked_simt_kernel(const __grid_constant__ MaskedParams p) {
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   const float inv = 1.f / l;
   // m and the scores are in log2 units
-  if (p.lse && lane == 0) p.lse[(size_t)h * p.lse_stride + row] = (m + log2f(l)) * 0.6931471805599453f;
+  if (out.lse && lane == 0) out.lse[(size_t)h * out.stride + row] = (m + log2f(l)) * 0.6931471805599453f;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) store_elem(O + row * hs + (size_t)h * D + lane + 32 * e, acc[e] * inv);
 }
 
 cudaError_t launch_masked_forward_simt(const MaskedParams& p, int elem, cudaStream_t stream) {
+  return launch_masked_forward_simt(p, elem, RowLse{nullptr, 0}, stream);
+}
+
+cudaError_t launch_masked_forward_simt(const MaskedParams& p, int elem, const RowLse& lse, cudaStream_t stream) {
   dim3 grid((p.L + kSimtWarps - 1) / kSimtWarps, p.H);
-  if (elem == kF32 && p.D == 64) masked_simt_kernel<float, 64><<<grid, kSimtWarps * 32, 0, stream>>>(p);
-  else if (elem == kF32 && p.D == 128) masked_simt_kernel<float, 128><<<grid, kSimtWarps * 32, 0, stream>>>(p);
-  else if (elem == kBF16 && p.D == 64) masked_simt_kernel<__nv_bfloat16, 64><<<grid, kSimtWarps * 32, 0, stream>>>(p);
-  else if (elem == kBF16 && p.D == 128) masked_simt_kernel<__nv_bfloat16, 128><<<grid, kSimtWarps * 32, 0, stream>>>(p);
+  if (elem == kF32 && p.D == 64) masked_simt_kernel<float, 64><<<grid, kSimtWarps * 32, 0, stream>>>(p, lse);
+  else if (elem == kF32 && p.D == 128) masked_simt_kernel<float, 128><<<grid, kSimtWarps * 32, 0, stream>>>(p, lse);
+  else if (elem == kBF16 && p.D == 64) masked_simt_kernel<__nv_bfloat16, 64><<<grid, kSimtWarps * 32, 0, stream>>>(p, lse);
+  else if (elem == kBF16 && p.D == 128) masked_simt_kernel<__nv_bfloat16, 128><<<grid, kSimtWarps * 32, 0, stream>>>(p, lse);
   else return cudaErrorInvalidValue;
   return cudaGetLastError();
 }

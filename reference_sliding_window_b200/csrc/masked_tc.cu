@@ -51,7 +51,7 @@
 #include <vector>
 
 #include "common.cuh"
-#include "internal.h"
+#include "masked_lse.h"
 #include "tc.cuh"
 
 namespace rswa {
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) masked_tc_kernel(const __grid_con
 // single-sequence form): every (document, pair of query tiles, head) is one
 // CTA.  Entries are ordered by their number of key tiles, heaviest first;
 // a pack with more than kMaxWork pairs is split over several launches.
-cudaError_t launch_masked_forward_tc(const MaskedParams& mp, cudaStream_t stream) {
+cudaError_t launch_masked_forward_tc(const MaskedParams& mp, const RowLse& lse, cudaStream_t stream) {
   using namespace tc;
   static TcParams p;  // 16 KB: built in static storage, copied by the launch
   static std::mutex mu;
@@ -601,8 +601,8 @@ cudaError_t launch_masked_forward_tc(const MaskedParams& mp, cudaStream_t stream
   p.scale_log2 = mp.scale_log2;
   p.bidir = mp.bidir_prefix;
   p.timing = mp.timing;
-  p.lse = mp.lse;
-  p.lse_stride = mp.lse_stride;
+  p.lse = lse.lse;
+  p.lse_stride = lse.stride;
   p.kc = static_cast<__nv_bfloat16*>(mp.fill_kc);
   p.vc = static_cast<__nv_bfloat16*>(mp.fill_vc);
   p.S_cap = mp.fill_S_cap;
@@ -634,6 +634,10 @@ cudaError_t launch_masked_forward_tc(const MaskedParams& mp, cudaStream_t stream
     }
   }
   return flush();
+}
+
+cudaError_t launch_masked_forward_tc(const MaskedParams& mp, cudaStream_t stream) {
+  return launch_masked_forward_tc(mp, RowLse{nullptr, 0}, stream);
 }
 
 }  // namespace rswa

@@ -15,7 +15,7 @@
 
 #include "rotary.h"
 
-#include "common.cuh"
+#include "launch.cuh"
 
 namespace rswa {
 namespace {
