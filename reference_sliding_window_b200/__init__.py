@@ -676,6 +676,8 @@ def masked_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int
     """masked_forward as a differentiable function of Q, K and V (once
     differentiable).  rotary: Q and K are turned first, to positions (int32
     [L] on the device; None: 0 .. L-1), and their gradients turned back."""
+    if rotary is None and positions is not None:
+        raise ValueError("positions without rotary")
     return _MaskedAttention.apply(Q, K, V, (0, Q.shape[0]), (int(L_m),), n, scale, bidir_prefix, rotary, positions)
 
 
@@ -685,6 +687,8 @@ def masked_attention_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, c
     """masked_forward_varlen as a differentiable function, as
     masked_attention.  rotary without positions: document_positions of the
     pack (pass them to reuse them over a model's layers or to capture)."""
+    if rotary is None and positions is not None:
+        raise ValueError("positions without rotary")
     if rotary is not None and positions is None:
         positions = document_positions(cu_seqlens, Q.device)
     cu, refs = tuple(int(x) for x in cu_seqlens), tuple(int(x) for x in ref_lens)

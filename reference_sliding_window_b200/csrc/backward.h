@@ -86,7 +86,7 @@ struct BackwardParams {
   int n_docs;
   // workspace
   float2* stats;    // [H][stat_stride]: (-lse log2 e, -delta) of each row
-  int stat_stride;  // at least L + 128: a tile's rows may reach past the pack
+  int stat_stride;  // L and a tile of padding
   float* partials;  // [parts][H][2][tile][D]
   int32_t* counter; // one per launch: items taken off its list, zeroed with the statistics
   int n_counters;

@@ -12,7 +12,7 @@ import torch
 
 import oracle
 from reference_sliding_window_b200 import (Rotary, RSWAError, _native, document_positions, masked_attention,
-                                           masked_backward, masked_forward, synth)
+                                           masked_attention_varlen, masked_backward, masked_forward, synth)
 from tests import gradients
 
 
@@ -111,6 +111,10 @@ def test_host_tensors_are_refused():
         masked_forward(x, x, x, L_m=2, n=1, return_lse=True)
     with pytest.raises(ValueError, match="CUDA"):
         masked_attention(x, x, x, L_m=2, n=1)
+    with pytest.raises(ValueError, match="rotary"):
+        masked_attention(x, x, x, L_m=2, n=1, positions=torch.arange(4))
+    with pytest.raises(ValueError, match="rotary"):
+        masked_attention_varlen(x, x, x, [0, 4], [2], 1, positions=torch.arange(4))
 
 
 def test_document_positions():
