@@ -20,7 +20,7 @@
 namespace rswa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 struct Turn {
   float c, s;
