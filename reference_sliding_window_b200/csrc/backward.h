@@ -73,6 +73,11 @@ __host__ __device__ inline BwdTiles bwd_query_tiles(int size, int tile, int len,
   return {0, first, last / size - first + 1};
 }
 
+// Every row of the document sees one key: its P is 1 whatever its score, and
+// dQ = dK = 0.  dS, the difference of two equal sums formed in two orders,
+// would leave their rounding error; such an item's scale is 0 instead.
+__host__ __device__ inline bool bwd_one_key(int len, int ref, int n) { return len == 1 || (ref == 0 && n == 1); }
+
 struct BackwardParams {
   const void *dO, *Q, *K, *V, *O;
   const float* lse;  // [H][L]

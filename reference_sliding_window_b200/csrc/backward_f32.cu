@@ -274,8 +274,8 @@ __device__ __forceinline__ void run_item(const F32Params& p, const BwdWork& w, i
     __syncthreads();
   }
   float* part = w.part < 0 ? nullptr : b.partials + (((size_t)w.part * b.H + h) * 2 + (DQ ? 0 : team)) * kT * D;
-  write_block<D, NT>(acc, DQ ? b.dQ : team ? b.dK : b.dV, part, DQ || team ? b.scale : 1.f, w.start + own0, end, b.H, h,
-                     gr, gc, g, t);
+  const float scale = !DQ && team == 0 ? 1.f : bwd_one_key(w.len, w.ref, b.n) ? 0.f : b.scale;
+  write_block<D, NT>(acc, DQ ? b.dQ : team ? b.dK : b.dV, part, scale, w.start + own0, end, b.H, h, gr, gc, g, t);
 }
 
 template <int D, int N>

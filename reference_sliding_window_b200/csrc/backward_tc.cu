@@ -554,7 +554,9 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     tmem_wait_ld();
     const bool good = ok && !ld_shared(bar0 + 8u * kSlotAbort);
     if (DQ || which == 1 || !good) {
-      const float mul = !good ? __int_as_float(0x7fc00000) : out.part < 0 ? p.b.scale : 1.f;
+      const float mul = !good ? __int_as_float(0x7fc00000)
+                        : out.part >= 0 ? 1.f
+                        : bwd_one_key(out.len, out.ref, p.b.n) ? 0.f : p.b.scale;
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] *= mul;
     }

@@ -104,6 +104,21 @@ def test_gradient_with_a_scale(scale, dtype, d):
     _check(*_inputs(333, 2, d, dtype, seed=4, gain=1.0), [0, 333], [120], 40, scale=scale)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cu,refs,n,bidir", [
+    ([0, 1], [1], 7, False),
+    ([0, 1], [1], 7, True),
+    ([0, 1, 2, 3], [0, 1, 0], 128, False),
+    ([0, 300], [0], 1, False),   # a window of one and no prefix
+])
+def test_rows_of_one_key_have_no_score_gradient(cu, refs, n, bidir, dtype, d):
+    """P = 1 whatever the score: dQ and dK are 0, not the rounding of dS."""
+    dO, Q, K, V = _inputs(cu[-1], 3, d, dtype, seed=11)
+    dQ, dK, _ = _check(dO, Q, K, V, cu, refs, n, bidir=bidir)
+    assert not dQ.any() and not dK.any()
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128)])
 def test_few_heads_and_long_sequences_split_their_sums(dtype, d):
     """One head: tiles with many partners are cut into shares whose sums are joined."""
