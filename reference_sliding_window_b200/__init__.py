@@ -555,6 +555,7 @@ class Rotary:
     def __call__(self, Q: torch.Tensor, K: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
                  first: int = 0):
         """apply as a differentiable function of Q and K."""
+        _check_capture(*((Q,) if K is None else (Q, K)))
         r = _Turn.apply(self, positions, first, *((Q,) if K is None else (Q, K)))
         return r[0] if K is None else r
 
@@ -622,14 +623,46 @@ class Rotary:
         return outs[0] if K is None else outs
 
 
+def _check_capture(*inputs) -> None:
+    """Refuses a differentiable call under stream capture whose backward pass
+    would add a leaf's gradient on the default stream, which a capture may not
+    reach: the backward pass would end the process.  A leaf's gradient stays
+    on the stream of the first autograd graph over it for as long as any graph
+    holds the leaf (a kept loss is enough)."""
+    if not (inputs[0].is_cuda and torch.is_grad_enabled() and torch.cuda.is_current_stream_capturing()):
+        return
+    todo, seen = [t.grad_fn for t in inputs if t.grad_fn is not None], set()
+    leaves = [t for t in inputs if t.grad_fn is None and t.requires_grad]
+    while todo:
+        node = todo.pop()
+        if node in seen:
+            continue
+        seen.add(node)
+        if hasattr(node, "variable"):
+            leaves.append(node.variable)
+        todo += [f for f, _ in node.next_functions if f is not None]
+    if any(_native.binding().accumulates_on_default_stream(t) for t in leaves):
+        raise ValueError("capture of a differentiable call while an autograd graph made on the default stream still "
+                         "holds one of its leaves: drop that graph's results first, or make it on a side stream")
+
+
 def document_positions(cu_seqlens: Sequence[int], device=None) -> torch.Tensor:
     """int32 positions of a pack's rows, each document from 0 on, on the
     device (copied from the host: not inside a graph capture)."""
     cu = np.asarray([int(x) for x in cu_seqlens], dtype=np.int64)
     if cu.size < 2 or cu[0] != 0 or (np.diff(cu) < 1).any():
         raise ValueError("cu_seqlens must start at 0 and increase")
+    if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+        raise ValueError("document_positions copies from the host: make them before the capture")
     pos = np.arange(cu[-1], dtype=np.int64) - np.repeat(cu[:-1], np.diff(cu))
     return torch.from_numpy(pos.astype(np.int32)).to(torch.device("cuda") if device is None else device)
+
+
+def _grad(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels read it: contiguous, on a 16-byte address
+    (that of a part of a concatenation may be neither)."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
 
 
 class _Turn(torch.autograd.Function):
@@ -644,7 +677,7 @@ class _Turn(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dQ, dK=None):
         positions, = ctx.saved_tensors
-        g = (dQ.contiguous(),) if dK is None else (dQ.contiguous(), dK.contiguous())
+        g = (_grad(dQ),) if dK is None else (_grad(dQ), _grad(dK))
         r = ctx.rotary.apply(*g, positions=positions, first=ctx.first, inverse=True)
         return (None, None, None) + ((r,) if dK is None else r)
 
@@ -664,7 +697,7 @@ class _MaskedAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
         Q, K, V, O, lse, positions = ctx.saved_tensors
-        dQ, dK, dV = masked_backward_varlen(dO.contiguous(), Q, K, V, O, lse, *ctx.args)
+        dQ, dK, dV = masked_backward_varlen(_grad(dO), Q, K, V, O, lse, *ctx.args)
         if ctx.rotary is not None:
             ctx.rotary.apply(dQ, dK, positions=positions, inverse=True, out=(dQ, dK))
         return (dQ, dK, dV) + (None,) * 7
@@ -678,6 +711,7 @@ def masked_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int
     [L] on the device; None: 0 .. L-1), and their gradients turned back."""
     if rotary is None and positions is not None:
         raise ValueError("positions without rotary")
+    _check_capture(Q, K, V)
     return _MaskedAttention.apply(Q, K, V, (0, Q.shape[0]), (int(L_m),), n, scale, bidir_prefix, rotary, positions)
 
 
@@ -691,5 +725,6 @@ def masked_attention_varlen(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, c
         raise ValueError("positions without rotary")
     if rotary is not None and positions is None:
         positions = document_positions(cu_seqlens, Q.device)
+    _check_capture(Q, K, V)
     cu, refs = tuple(int(x) for x in cu_seqlens), tuple(int(x) for x in ref_lens)
     return _MaskedAttention.apply(Q, K, V, cu, refs, n, scale, bidir_prefix, rotary, positions)

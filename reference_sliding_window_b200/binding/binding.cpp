@@ -19,7 +19,9 @@
 #include <c10/cuda/CUDAStream.h>
 #include <c10/util/SmallVector.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/function.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/variable.h>
 
 #include "rswa.h"
 
@@ -193,10 +195,23 @@ PyObject* rotary(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// (leaf) -> whether its gradient is added up on its device's default stream:
+// an autograd graph made there still holds the leaf.
+PyObject* accumulates_on_default_stream(PyObject*, PyObject* leaf) {
+  const at::Tensor* t = THPVariable_Check(leaf) ? &THPVariable_Unpack(leaf) : nullptr;
+  if (!t || !t->is_cuda()) Py_RETURN_FALSE;
+  HANDLE_TH_ERRORS
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(*t);
+    const auto stream = node ? node->stream() : std::nullopt;
+    return PyBool_FromLong(stream && *stream == c10::cuda::getDefaultCUDAStream(t->device().index()).unwrap());
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(backward)), METH_FASTCALL, nullptr},
     {"rotary", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rotary)), METH_FASTCALL, nullptr},
+    {"accumulates_on_default_stream", accumulates_on_default_stream, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -272,6 +272,29 @@ def test_attention_of_one_document_and_expanded_gradients():
     assert_gradients((Q.grad, V.grad), (want[0], want[2]), (bounds[0], bounds[2]))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_off_a_16_byte_address(dtype):
+    """The gradient of a part of a concatenation starts anywhere."""
+    L, L_m, n, H, d = 70, 20, 9, 2, 64
+    dO, Q, K, V = _inputs(L, H, d, dtype, seed=27)
+    leaves = [t.clone().requires_grad_() for t in (Q, K, V)]
+    rot = Rotary(d)
+    pad = torch.zeros(1, device="cuda", dtype=Q.dtype)
+
+    def grads(off):
+        q, k = rot(*leaves[:2])
+        q, k = ((torch.cat([pad, t.flatten()])[1:].clone().view_as(t) if off else t) for t in (q, k))
+        O = masked_attention(q, k, leaves[2], L_m=L_m, n=n)
+        if off:
+            loss = (torch.cat([pad, O.flatten()]) * torch.cat([pad, dO.flatten()])).sum()
+        else:
+            loss = (O * dO).sum()
+        return torch.autograd.grad(loss, leaves)
+
+    for x, y in zip(grads(False), grads(True)):
+        assert torch.equal(x, y)
+
+
 def test_backward_on_another_stream_and_captured():
     """On a side stream, and captured once and replayed on new inputs; two
     graphs keep their own workspaces."""
@@ -302,6 +325,67 @@ def test_backward_on_another_stream_and_captured():
             for x, y in zip(outs, want):
                 assert torch.equal(x, y)
         assert not torch.equal(first[0], want[0])
+
+
+def _captured_step(seed):
+    """Static leaves, and one training step over them (a pack, with positions)."""
+    cu, refs, n, d = [0, 150, 333], [90, 40], 25, 64
+    dO, Q, K, V = _inputs(cu[-1], 2, d, "bf16", seed=seed)
+    leaves = [t.clone().requires_grad_() for t in (Q, K, V)]
+    rot, pos = Rotary(d), document_positions(cu)
+
+    def step():
+        O = masked_attention_varlen(*(t * 1.0 for t in leaves), cu, refs, n, rotary=rot, positions=pos)
+        return torch.autograd.grad((O * dO).sum(), leaves)
+
+    return leaves, dO, step
+
+
+def test_training_step_captured():
+    """Forward and backward in one graph, replayed on new inputs."""
+    leaves, dO, step = _captured_step(70)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = step()
+    for seed in (71, 72):
+        for t, x in zip((dO, *leaves), _inputs(leaves[0].shape[0], 2, 64, "bf16", seed=seed)):
+            t.data.copy_(x)
+        g.replay()
+        want = step()
+        torch.cuda.synchronize()
+        for x, y in zip(outs, want):
+            assert torch.equal(x, y)
+
+
+def test_capture_is_refused_while_an_eager_graph_lives():
+    """A result kept on the default stream holds the leaves: refused in the
+    forward call, before the backward pass could end the process."""
+    leaves, _, step = _captured_step(80)
+    kept = sum(t.float().sum() for t in leaves)
+    side = torch.cuda.Stream()
+    rot, a = Rotary(64), torch.zeros(1, device="cuda")
+    with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+        a.add_(1)
+        with pytest.raises(ValueError, match="default stream"):
+            step()
+        with pytest.raises(ValueError, match="default stream"):
+            rot(leaves[0])
+        with pytest.raises(ValueError, match="before the capture"):
+            document_positions([0, 3])
+        with torch.no_grad():
+            rot(leaves[0])
+    del kept
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        outs = step()
+    g.replay()
+    for x, y in zip(outs, step()):
+        assert torch.equal(x, y)
 
 
 def test_decode_after_a_turned_prefill():
