@@ -6,10 +6,12 @@
 // takes the leading 11 bits; x y is taken as hi hi + hi lo + lo hi, accumulated
 // in float32.  |lo| is at most 2^-11 |x|, so lo's cut leaves 2^-21 |x| and the
 // dropped lo lo 2^-22 |x y|: a product is off by at most 1.25 2^-20, a few
-// float32 roundings (rounding lo too would cost one more conversion per
-// element, 792 against 712 us for 2011 rows, 10 heads, d = 128).  Plain FMAs
-// are bound by shared memory, not by the FMA pipes: the register file takes 128
-// bytes a cycle from it, half of what 4x4 blocks a thread need (925 us).
+// float32 roundings.  Plain FMAs are bound by shared memory, not by the FMA
+// pipes: the register file takes 128 bytes a cycle from it, half of what 4x4
+// blocks a thread need (2011 rows, 10 heads, d = 128: 925 us, this kernel 605).
+// The tensor pipe is busy 53 % of that time (its rate for these MMAs, 1024
+// operations a cycle and SM, measured); loading the next tiles under this pair's
+// work saved under 1 %, so they are loaded plainly.
 //
 // One CTA of 16 warps per work item and head, tiles of 64 queries x 64 keys.
 // Per tile pair warps 0-7 form S (32 x 16 each) and write P to shared memory,
@@ -66,7 +68,9 @@ struct Split {
 };
 __device__ __forceinline__ Split split(float x) {
   Split s;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(s.hi) : "f"(x));
+  // to the nearest 11 bits, in integers (605 us; with the conversion
+  // instruction 675).  A NaN may be lost here, but lo keeps it.
+  s.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   s.lo = __float_as_uint(x - __uint_as_float(s.hi));
   return s;
 }
