@@ -481,6 +481,14 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
       mask(x, len, ref);
       past_end = o0 + kTile > len;
       if (past_end) {  // rows of the streamed tiles past the document's end
+        // The tile on ring A has landed: S, complete, has read it.  Nothing so
+        // far says that of the dO tile on ring B, and a load that landed after
+        // the clear would bring the next document's rows back.  Its stage is
+        // filled again only after dV(j), which waits for this warp's P: the
+        // phase that is waited for cannot be overtaken.  dP(j) may read the
+        // tile before, under or after the clear: these rows are its columns of
+        // masked pairs alone, and dP is zeroed there below whatever it holds.
+        if (!DQ) wait(kBarBFull + it % nB, it / nB);
         const int valid = len - o0;
         for (int i = tid - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
           const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);

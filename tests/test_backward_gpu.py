@@ -190,6 +190,29 @@ def test_documents_do_not_touch_each_other(bad, dtype, d):
         assert torch.equal(x[:200], y[:200]) and torch.equal(x[330:], y[330:])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_documents_whose_tiles_come_from_memory_do_not_touch_each_other(d):
+    """Thousands of documents shorter than a tile, ten heads, several times
+    what L2 holds, and NaN in the dO of every second one: the clean ones keep
+    their bits, call after call.  Every document's tiles reach over the next
+    one's rows, and each of an item's loads may land at any time."""
+    H, n, docs = 10, 40, 2400 if d == 64 else 1200
+    rng = np.random.default_rng(d)
+    sizes = rng.integers(1, 128, size=docs)
+    cu = [0] + np.cumsum(sizes).tolist()
+    refs = [int(rng.integers(0, s + 1)) for s in sizes]
+    g = torch.Generator(device="cuda").manual_seed(d)
+    dO, Q, K, V = (torch.randn((cu[-1], H, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(4))
+    O, lse = masked_forward_varlen(Q, K, V, cu, refs, n, return_lse=True)
+    clean = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n)
+    rows = torch.from_numpy(np.repeat(np.arange(docs) % 2 == 0, sizes)).cuda()
+    dO[~rows] = float("nan")
+    for _ in range(5):
+        got = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n)
+        for name, x, y in zip(("dQ", "dK", "dV"), got, clean):
+            assert torch.equal(x[rows], y[rows]), name
+
+
 def test_gradient_32k_sampled():
     """The 32768-row teacher-forced sequence (12832 reference rows, 10 heads,
     bf16): rows of dQ, dK and dV on the mask's edges and at random, against
