@@ -308,8 +308,9 @@ rswa_status rswa_masked_forward_lse(const void* Q, const void* K, const void* V,
  * Every gradient element is summed in one fixed order in float32: the same
  * call gives the same bits.  An infinity or a NaN in one document leaves the
  * others' gradients as they are.  Every argument is checked before anything is
- * enqueued; the host arrays are read during the call only.  Should a kernel's
- * bounded wait run out, the rows that it worked on are NaN. */
+ * enqueued; the host arrays are read during the call only.  Should a bounded
+ * wait of the BF16 kernel run out, the rows that it affects, those of work
+ * not begun among them, are NaN. */
 size_t rswa_masked_backward_workspace_bytes(const int32_t* cu_seqlens, const int32_t* ref_lens, int n_docs, int n,
                                             int H, int d, rswa_dtype dtype, int flags);
 rswa_status rswa_masked_backward(const void* dO, const void* Q, const void* K, const void* V, const void* O,

@@ -156,7 +156,11 @@ __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constan
   }
 }
 
+thread_local int give_up_ctas = 0;
+
 }  // namespace
+
+extern "C" void rswa_testing_backward_give_up(int ctas) { give_up_ctas = ctas; }
 
 size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_docs, int n, int H, int D, int elem,
                                 bool bidir) {
@@ -171,6 +175,7 @@ cudaError_t launch_backward(BackwardParams p, int elem, void* workspace, cudaStr
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.counter = reinterpret_cast<int32_t*>(ws);
   p.n_counters = n_launches(plan);
+  p.give_up = give_up_ctas;
   p.stats = reinterpret_cast<float2*>(ws + counter_bytes(plan));
   p.stat_stride = p.L + 128;
   p.partials = reinterpret_cast<float*>(ws + counter_bytes(plan) + stats_bytes(p.L, p.H));

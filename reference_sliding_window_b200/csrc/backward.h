@@ -95,6 +95,7 @@ struct BackwardParams {
   float* partials;  // [parts][H][2][tile][D]
   int32_t* counter; // one per launch: items taken off its list, zeroed with the statistics
   int n_counters;
+  int give_up;      // CTAs of the bf16 kernel whose waits run out at once (tests)
 };
 
 constexpr int kBwdTileTc = 128, kBwdTileF32 = 64;
@@ -106,6 +107,11 @@ template <typename Common, int N>
 struct BwdLaunch : Common {
   BwdWork work[N];  // heaviest first
 };
+
+// Failure injection for the tests of the bf16 kernel's bounded waits: in the
+// calling thread's gradient calls from here on, each launch's first `ctas` CTAs
+// behave as if a wait had run out.  0, the default: none.
+extern "C" void rswa_testing_backward_give_up(int ctas);
 
 size_t backward_workspace_bytes(const int32_t* cu, const int32_t* refs, int n_docs, int n, int H, int D, int elem,
                                 bool bidir);

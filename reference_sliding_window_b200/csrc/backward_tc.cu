@@ -42,8 +42,9 @@
 //   us, as long as a short document's whole item): every role walks the items
 //   by itself, and barriers, not the CTA's start, order one item's use of a tile,
 //   a region or an accumulator before the next one's.
-// * Every wait is bounded; on a timeout the rows of the CTA's items are written
-//   as NaN.
+// * Every wait is bounded.  A CTA in which one ran out writes the rows of the
+//   items that it holds as NaN, and then those of every item still on the list
+//   (which other CTAs may not live to take): no row keeps what was there before.
 
 #include <algorithm>
 
@@ -113,7 +114,8 @@ enum : int {
   kBarStats = 35,     // 2 (dK, dV items)
   kBarStatsFree = 37, // 2
   kBarEnd = 39,
-  kSlotTmem = 40, kSlotAbort = 41, kSlotItem = 42  // 2 x 64 bytes: Item::Slot
+  kSlotTmem = 40, kSlotAbort = 41, kSlotItem = 42,  // 2 x 64 bytes: Item::Slot
+  kSlotLeft = 58      // an item that was taken and not announced, or -1
 };
 
 constexpr uint32_t idesc(int n, bool b_n_major) {
@@ -600,6 +602,20 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
   arrive(kBarAccFree);
 }
 
+// What an item would have written, as NaN (all threads of the CTA).
+__device__ __forceinline__ void write_nan(const BwdWork& w, int h, const BackwardParams& b) {
+  const int first = w.tile * kTile, rows = w.part >= 0 ? kTile : min(kTile, w.len - first);
+  for (int which = 0; which < (w.kind == kBwdDQ ? 1 : 2); ++which) {
+    __nv_bfloat16* grad = static_cast<__nv_bfloat16*>(w.kind == kBwdDQ ? b.dQ : which == 0 ? b.dV : b.dK) +
+                          ((size_t)(w.start + first) * b.H + h) * b.D;
+    float* part = b.partials + (((size_t)max(w.part, 0) * b.H + h) * 2 + which) * kTile * b.D;
+    for (int i = threadIdx.x; i < rows * b.D; i += kThreads) {
+      if (w.part >= 0) part[i] = __int_as_float(0x7fc00000);
+      else grad[(size_t)(i / b.D) * b.H * b.D + i % b.D] = __ushort_as_bfloat16(0x7fc0);
+    }
+  }
+}
+
 template <int D, int N>
 __global__ void __launch_bounds__(kThreads, 1)
     backward_tc_kernel(const __grid_constant__ BwdLaunch<BwdTcParams, N> p) {
@@ -628,7 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the roles that read an item's number: MMA, statistics, softmax
       mbar_init(B(s), per_warp ? kWarps : s == kBarItemFree || s == kBarItemFree + 1 ? kWarps + 2 : 1);
     }
-    *s_abort = (sbase & 1023) != 0;
+    *s_abort = (sbase & 1023) != 0 || (int)blockIdx.x < p.b.give_up;
+    st_shared(Item::slot(bar0, 1), -1);
+    st_shared(B(kSlotLeft), -1);
     fence_barrier_init();
   }
   const uint32_t smA = sbase + C::kSmA, smB = sbase + C::kSmB, smRes = sbase + C::kSmRes;
@@ -706,7 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         if (k > 0) {
           ok = wait(kBarItemFree + (k & 1), (k >> 1) + 1);
-          if (!ok) break;
+          if (!ok) {
+            st_shared(B(kSlotLeft), item.number);
+            break;
+          }
           announce(k);
           if (item.number < 0) break;
         }
@@ -724,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           load_b(j);
         }
+        if (!ok) break;
         item.T += item.nt;
         if (item.dq) ++item.kq;
         else item.U += item.nt;
@@ -874,6 +896,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                               : "memory");
+  if (*s_abort) {
+    // The two announced last may be unfinished (one is announced when every role
+    // is done with the one before the last), one may be taken and not announced.
+    dependency_wait();
+    const uint32_t held[3] = {Item::slot(bar0, 0), Item::slot(bar0, 1), B(kSlotLeft)};
+    for (uint32_t slot : held) {
+      const int number = ld_shared(slot);
+      if (number >= 0 && number < p.n_items) write_nan(p.work[number / p.b.H], number % p.b.H, p.b);
+    }
+    while (true) {
+      __syncthreads();
+      if (threadIdx.x == 0) st_shared(B(kSlotLeft), (int)gridDim.x + atomicAdd(p.b.counter, 1));
+      __syncthreads();
+      const int number = ld_shared(B(kSlotLeft));
+      if (number >= p.n_items) break;
+      write_nan(p.work[number / p.b.H], number % p.b.H, p.b);
+    }
+  }
 }
 
 template <int D, int N>

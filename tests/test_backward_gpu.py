@@ -4,13 +4,15 @@ roundings (tests/gradients.py)."""
 
 from __future__ import annotations
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 from reference_sliding_window_b200 import (RSWA, Rotary, RSWAError, document_positions, masked_attention,
                                            masked_attention_varlen, masked_backward, masked_backward_varlen,
-                                           masked_forward, masked_forward_varlen, synth)
+                                           masked_forward, masked_forward_varlen, synth, _native)
 from tests import gradients
 from tests.gradients import assert_gradients
 
@@ -211,6 +213,39 @@ def test_short_documents_whose_tiles_come_from_memory_do_not_touch_each_other(d)
         got = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n)
         for name, x, y in zip(("dQ", "dK", "dV"), got, clean):
             assert torch.equal(x[rows], y[rows]), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ctas", [10 ** 6, 1, 40])
+def test_rows_of_a_kernel_that_gives_up_are_nan(ctas, d):
+    """Waits that run out (injected on the host) leave no row as it was: the
+    items that the CTAs held, had taken without starting them, or never took
+    are NaN, the others right; split sums too.  The next call is right again."""
+    give_up = _native.lib().rswa_testing_backward_give_up
+    give_up.argtypes, give_up.restype = [ctypes.c_int], None
+    rng = np.random.default_rng(ctas)
+    short = np.cumsum(rng.integers(1, 200, size=400)).tolist()
+    for cu, refs, H in (([0, 3000], [2500], 1),        # every item in shares
+                        ([0, 700, 1001], [288, 30], 3),  # fewer items than CTAs
+                        ([0] + short, [0] * len(short), 4)):  # many short items a CTA, two launches
+        dO, Q, K, V = _inputs(cu[-1], H, d, "bf16", seed=33)
+        O, lse = masked_forward_varlen(Q, K, V, cu, refs, 64, return_lse=True)
+        want = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, 64)
+        out = tuple(torch.full_like(Q, 7.0) for _ in range(3))
+        try:
+            give_up(ctas)
+            got = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, 64, out=out)
+        finally:
+            give_up(0)
+        torch.cuda.synchronize()
+        assert any(x.isnan().any() for x in got)
+        for x, y in zip(got, want):
+            if ctas >= 1000:
+                assert x.isnan().all()
+            else:
+                assert torch.where(x.isnan(), y, x).equal(y)
+        for x, y in zip(masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, 64), want):
+            assert torch.equal(x, y)
 
 
 def test_gradient_32k_sampled():
