@@ -92,15 +92,18 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             todo.append((s, o))
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with cf.ThreadPoolExecutor(max_workers=min(8, len(todo) + 1)) as ex:
-        for f in [ex.submit(build_binding, force)] + [ex.submit(_compile, s, o, extra) for s, o in todo]:
+        binding = ex.submit(build_binding, force)
+        for f in [ex.submit(_compile, s, o, extra) for s, o in todo]:
             f.result()
-    if todo or not os.path.exists(LIB):
-        tmp = LIB + ".tmp"
-        cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
-        os.replace(tmp, LIB)
+        if todo or not os.path.exists(LIB):
+            tmp = LIB + ".tmp"
+            cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
+            os.replace(tmp, LIB)
+        # The library needs nothing of torch: it is there, whatever becomes of the binding.
+        binding.result()
     return LIB
 
 
