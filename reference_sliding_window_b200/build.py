@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -59,9 +60,16 @@ def _compile(src: str, obj: str, extra) -> None:
         sys.stderr.write(r.stderr)
 
 
+def _binding_abi() -> str:
+    return f"torch {importlib.metadata.version('torch')}, {sysconfig.get_config_var('SOABI')}"
+
+
 def build_binding(force: bool = False) -> None:
     deps = (BINDING_SRC, os.path.join(INCLUDE, "rswa.h"))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+    # It is bound to the ABI of the torch and the Python that it was compiled for.
+    stamp, made_for = os.path.join(BUILD, "binding.stamp"), _binding_abi()
+    if (not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps))
+            and os.path.exists(stamp) and open(stamp).read() == made_for):
         return
     import torch
 
@@ -78,6 +86,8 @@ def build_binding(force: bool = False) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"binding.cpp failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(made_for)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:

@@ -36,3 +36,20 @@ def test_the_library_is_linked_whatever_becomes_of_the_binding(faked, monkeypatc
     with pytest.raises(ImportError, match="no torch"):
         b.build()
     assert os.path.exists(b.LIB)
+
+
+def test_the_binding_is_rebuilt_for_another_torch_or_python(faked, monkeypatch):
+    def binding_builds():
+        faked.clear()
+        b.build()
+        return sum(b.BINDING_SRC in cmd for cmd in faked)
+
+    assert binding_builds() == 1
+    assert binding_builds() == 0
+    monkeypatch.setattr(b.importlib.metadata, "version", lambda _: "0.0")
+    assert binding_builds() == 1
+    assert binding_builds() == 0
+    monkeypatch.setattr(b.sysconfig, "get_config_var", lambda _: "cpython-00")
+    assert binding_builds() == 1
+    os.utime(b.BINDING, (0, 0))
+    assert binding_builds() == 1
