@@ -546,7 +546,7 @@ class Rotary:
                                              int(original_length)))
         self.mscale = self._plan.mscale
         self._ref, self._address = C.byref(self._plan), C.addressof(self._plan)
-        self._rotary = _native.binding().rotary
+        self._rotary = None  # the binding's function, from the first turn on: a plan alone needs no GPU build of torch
         self._made_from = (d, rotary_dim, base, interleaved, scaling, factor, original_length)
 
     def __reduce__(self):  # copies and pickles are made anew: the plan's address is this object's own
@@ -585,6 +585,8 @@ class Rotary:
         result, or the pair) may be such slices too, or the inputs
         themselves.  Returns Q's result, or the pair."""
         if out is None:
+            if self._rotary is None:
+                self._rotary = _native.binding().rotary
             r = self._rotary(self._address, Q, K, positions, first, inverse)
             if r.__class__ is int:
                 check(r)

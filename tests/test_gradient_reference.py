@@ -103,6 +103,16 @@ def test_rotary_plan_refusals():
         Rotary(64).apply(torch.zeros(3, 2, 64))
 
 
+def test_a_plan_needs_the_library_alone(monkeypatch):
+    def missing():
+        raise ImportError("no binding")
+    monkeypatch.setattr(_native, "binding", missing)
+    r = Rotary(64, scaling="linear", factor=2.0)
+    assert r.mscale == 1.0 and r._plan.turn[0] > 0
+    with pytest.raises(ImportError, match="no binding"):
+        r.apply(torch.zeros(3, 2, 64))
+
+
 def test_host_tensors_are_refused():
     x, lse = torch.zeros(4, 1, 64), torch.zeros(1, 4)
     with pytest.raises(ValueError, match="CUDA"):
