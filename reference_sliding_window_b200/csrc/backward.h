@@ -73,10 +73,14 @@ __host__ __device__ inline BwdTiles bwd_query_tiles(int size, int tile, int len,
   return {0, first, last / size - first + 1};
 }
 
-// Every row of the document sees one key: its P is 1 whatever its score, and
-// dQ = dK = 0.  dS, the difference of two equal sums formed in two orders,
-// would leave their rounding error; such an item's scale is 0 instead.
-__host__ __device__ inline bool bwd_one_key(int len, int ref, int n) { return len == 1 || (ref == 0 && n == 1); }
+// The first so many of a document's rows see one key (its first row, unless a
+// bidirectional prefix shows it more; every row of a window of one without a
+// prefix): P is 1 whatever the score, so dS = 0.  The difference of two equal sums
+// formed in two orders would leave their rounding error; the kernels set such a
+// row's dS to 0.  A tile with such a pair is never visible as a whole.
+__host__ __device__ inline int bwd_one_key_rows(int len, int ref, int n, bool bidir) {
+  return ref == 0 && n == 1 ? len : bidir && ref > 1 ? 0 : 1;
+}
 
 struct BackwardParams {
   const void *dO, *Q, *K, *V, *O;

@@ -270,6 +270,12 @@ __device__ __forceinline__ void run_item(const F32Params& p, const BwdWork& w, i
           const float y = team ? s[m][n][i] + x : exp2f(fmaf(s[m][n][i], p.scale_log2, x));
           mine[DQ ? r * kPS + c : c * kPS + r] = vis ? y : 0.f;
         }
+    if (!full && team && q0 < bwd_one_key_rows(w.len, w.ref, b.n, bidir)) {  // (the same elements again)
+      const int one_key = bwd_one_key_rows(w.len, w.ref, b.n, bidir) - q0;
+#pragma unroll 1
+      for (int r = sq + g; r < min(sq + 32, one_key); r += 8)
+        for (int c = sk + 2 * t; c < sk + 16; c += (c & 1) ? 7 : 1) mine[DQ ? r * kPS + c : c * kPS + r] = 0.f;
+    }
     __syncthreads();
     const float *w1 = t0 + gr * kPS, *w2 = t1 + gr * kPS;
     if (DQ) gradient<D, NT, true>(acc, w1, w2, str0 + gc, g, t);
@@ -278,7 +284,7 @@ __device__ __forceinline__ void run_item(const F32Params& p, const BwdWork& w, i
     __syncthreads();
   }
   float* part = w.part < 0 ? nullptr : b.partials + (((size_t)w.part * b.H + h) * 2 + (DQ ? 0 : team)) * kT * D;
-  const float scale = !DQ && team == 0 ? 1.f : bwd_one_key(w.len, w.ref, b.n) ? 0.f : b.scale;
+  const float scale = !DQ && team == 0 ? 1.f : b.scale;
   write_block<D, NT>(acc, DQ ? b.dQ : team ? b.dK : b.dV, part, scale, w.start + own0, end, b.H, h, gr, gc, g, t);
 }
 

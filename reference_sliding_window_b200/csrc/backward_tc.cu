@@ -46,6 +46,8 @@
 //   items that it holds as NaN, and then those of every item still on the list
 //   (which other CTAs may not live to take): no row keeps what was there before.
 
+#include <math.h>
+
 #include <algorithm>
 
 #include "backward.h"
@@ -405,11 +407,13 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
   dependency_wait();
   float nlse[4], ndelta[4];
   if (DQ) {
+    const int one_key = bwd_one_key_rows(w.len, w.ref, p.b.n, bidir);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 st = own0 + 8 * i < w.len ? p.b.stats[(size_t)w.h * p.b.stat_stride + w.start + own0 + 8 * i]
                                              : make_float2(0.f, 0.f);
-      nlse[i] = st.x;
+      // (a row that sees one key has no dS, and P serves nothing else here)
+      nlse[i] = own0 + 8 * i < one_key ? -INFINITY : st.x;
       ndelta[i] = st.y;
     }
   }
@@ -482,7 +486,20 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
       const int len = ld_shared(slot + 20), ref = ld_shared(slot + 24);
       mask(x, len, ref);
       past_end = o0 + kTile > len;
+      // Rows [from, to) of a streamed tile cleared in shared memory.
+      auto clear = [&](int stage, int from, int to) {
+        for (int i = tid - kSoftmaxWarp * 32; i < (to - from) * 8 * C::kBoxes; i += kSoftmaxThreads) {
+          const int row = from + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           bar0 - C::kSmBar + stage + (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16),
+                       "r"(0)
+                       : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      };
+      const int stage_a = C::kSmA + (it % nA) * C::kTileBytes;
       if (past_end) {  // rows of the streamed tiles past the document's end
+        clear(stage_a, len - o0, kTile);
         // The tile on ring A has landed: S, complete, has read it.  Nothing so
         // far says that of the dO tile on ring B, and a load that landed after
         // the clear would bring the next document's rows back.  Its stage is
@@ -490,20 +507,15 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
         // phase that is waited for cannot be overtaken.  dP(j) may read the
         // tile before, under or after the clear: these rows are its columns of
         // masked pairs alone, and dP is zeroed there below whatever it holds.
-        if (!DQ) wait(kBarBFull + it % nB, it / nB);
-        const int valid = len - o0;
-        for (int i = tid - kSoftmaxWarp * 32; i < (kTile - valid) * 8 * C::kBoxes; i += kSoftmaxThreads) {
-          const int row = valid + i / (8 * C::kBoxes), chunk = i % (8 * C::kBoxes);
-          const int off = (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16;
-          auto clear = [&](uint32_t stage) {
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(bar0 - C::kSmBar + stage + off), "r"(0)
-                         : "memory");
-          };
-          clear(C::kSmA + (it % nA) * C::kTileBytes);
-          if (!DQ) clear(C::kSmB + (it % nB) * C::kTileBytes);
+        if (!DQ) {
+          wait(kBarBFull + it % nB, it / nB);
+          clear(C::kSmB + (it % nB) * C::kTileBytes, len - o0, kTile);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       }
+      // Queries that see one key: dS = 0 in effect, as dK, the last to read their
+      // rows of Q, finds zeros there.
+      if (!DQ && (o0 == 0 || p.b.n == 1))
+        clear(stage_a, 0, min(kTile, bwd_one_key_rows(len, ref, p.b.n, bidir) - o0));
     }
     if (!DQ) {
       tmem_st_frag(tS, x);
@@ -565,8 +577,7 @@ __device__ __forceinline__ void softmax_item(uint32_t bar0, uint32_t tmem, const
     const bool good = ok && !ld_shared(bar0 + 8u * kSlotAbort);
     if (DQ || which == 1 || !good) {
       const float mul = !good ? __int_as_float(0x7fc00000)
-                        : out.part >= 0 ? 1.f
-                        : bwd_one_key(out.len, out.ref, p.b.n) ? 0.f : p.b.scale;
+                        : out.part >= 0 ? 1.f : p.b.scale;
 #pragma unroll
       for (int e = 0; e < 32; ++e) o[e] *= mul;
     }

@@ -121,6 +121,34 @@ def test_rows_of_one_key_have_no_score_gradient(cu, refs, n, bidir, dtype, d):
     assert not dQ.any() and not dK.any()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cu,refs,n,bidir", [
+    ([0, 300, 301, 500], [100, 1, 0], 16, False),
+    ([0, 2, 300], [2, 290], 16, False),
+    ([0, 130, 300, 430], [1, 0, 0], 5, True),   # a bidirectional prefix of one row, none
+    ([0, 3000], [2500], 128, False),            # tiles whose sums are split (with one head)
+])
+def test_a_document_s_first_row_has_no_score_gradient(cu, refs, n, bidir, dtype, d):
+    """It sees itself alone, in a document of any shape: its dQ is 0, and its
+    dO moves nothing but dV."""
+    H = 1 if cu[-1] == 3000 else 3
+    dO, Q, K, V = _inputs(cu[-1], H, d, dtype, seed=15)
+    O, lse = masked_forward_varlen(Q, K, V, cu, refs, n, bidir_prefix=bidir, return_lse=True)
+    dQ, dK, dV = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n, bidir_prefix=bidir)
+    assert not dQ[cu[:-1]].any()
+    dO[cu[:-1]] *= 8.0
+    other = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n, bidir_prefix=bidir)
+    assert torch.equal(dQ, other[0]) and torch.equal(dK, other[1])
+    assert not torch.equal(dV, other[2])
+
+
+def test_a_bidirectional_prefix_gives_the_first_row_its_gradient():
+    for dtype, d in (("bf16", 64), ("bf16", 128), ("f32", 64)):
+        dQ, _, _ = _check(*_inputs(400, 2, d, dtype, seed=16), [0, 150, 400], [2, 200], 16, bidir=True)
+        assert dQ[[0, 150]].any(-1).all()
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128)])
 def test_few_heads_and_long_sequences_split_their_sums(dtype, d):
     """One head: tiles with many partners are cut into shares whose sums are joined."""
