@@ -115,3 +115,72 @@ def rotary_bound(x, want, m=1.0):
     at most the head's largest element times sqrt 2."""
     size = m * math.sqrt(2.0) * x.double().abs().amax(-1, keepdim=True)
     return 2.0 ** -21 * size + 1.01 * U[x.dtype] * want.abs()
+
+
+# Norms.  The bounds above add every rounding at its largest and with one sign,
+# so an element of a long sum may be far off within them.  A block's norm may
+# not: roundings are independent and as often up as down, so that of a sum of
+# rounded terms grows as the root of the sum of their squares.  A rounding to
+# half a step, relative error at most u, has a root mean square of at most
+# s = u / sqrt 3 (uniform within the half step).
+# * The results are rounded once: s |x|.
+# * For the products P and dS are rounded to bf16 (low = s), or split for three
+#   tf32 products, off by 1.25 2^-20 at most (low = R = 2^-19, which covers the
+#   rounding of float32 sums of up to 1000 terms too: sqrt(1000) 2^-24 < 2^-19).
+# * Scores and dP are float32 sums of such products: R sqrt(sum of squared terms)
+#   each; the exponential and its argument's rounding: 2^-21 of P.
+# * delta_i gets one error for all of row i, of variance
+#   D_i = sum_c g_ic^2 ((s^2 + R^2) O_ic^2 + sum_j (P_ij v_jc)^2 (P's relative variance)):
+#   dQ_i is off by it along sum_j P_ij k_j, dK_j by P_ij of it along q_i.  (The
+#   row's lse likewise moves all of its P, by 2^-21 at most here.)
+# The norm over a block of 64 rows or more is held to three times its root mean
+# square: even where one row's delta carries most of it (a first row of few
+# keys), a normal error is beyond that once in 370 times at the variance above,
+# which is that of the worst mantissas (half of it on average).
+BLOCK = 64
+R = 2.0 ** -19
+
+
+def block_errors(dO, Q, K, V, cu, refs, n, scale=0.0, bidir=False):
+    """-> ((dQ, dK, dV), (their errors' root mean square per row and head)):
+    float64 [L, H, d] and [L, H]."""
+    vis = visible(cu, refs, n, bidir, Q.device)
+    d = Q.shape[-1]
+    sc = scale if scale > 0 else 1.0 / math.sqrt(d)
+    s = U[Q.dtype] / math.sqrt(3.0)
+    low = s if Q.dtype == torch.bfloat16 else R
+    grads, errors = [], []
+    for h in range(Q.shape[1]):
+        q, k, v, g = (t[:, h].double() for t in (Q, K, V, dO))
+        qq, kk, vv, gg = (t * t for t in (q, k, v, g))
+        S = (q @ k.T * sc).masked_fill(~vis, -math.inf)
+        lse = torch.logsumexp(S, -1, keepdim=True)
+        P = (S - lse).exp()
+        O = P @ v
+        dS = P * (g @ v.T - (O * g).sum(-1, keepdim=True))
+        out = (sc * dS @ k, sc * dS.T @ q, P.T @ g)
+        before = (R * sc) ** 2 * (qq @ kk.T) + 2.0 ** -42  # relative variance of P before its rounding
+        varP = P * P * (before + low * low)
+        D = (gg * ((s * s + R * R) * O * O + varP @ vv)).sum(-1)
+        vardS = dS * dS * (before + low * low) + P * P * R * R * (gg @ vv.T)
+        var = (sc * sc * (vardS @ kk.sum(-1) + D * (P @ k).square().sum(-1)),
+               sc * sc * (vardS.T @ qq.sum(-1) + (P * P).T @ (D * qq.sum(-1))),
+               varP.T @ gg.sum(-1))
+        grads.append(out)
+        errors.append([(a + (s * s + R * R) * x.square().sum(-1)).sqrt() for a, x in zip(var, out)])
+    return tuple(torch.stack(x, 1) for x in zip(*grads)), tuple(torch.stack(x, 1) for x in zip(*errors))
+
+
+def blocks(cu):
+    """Runs of at least BLOCK rows of one document (the last takes what is left)."""
+    for a, b in zip(cu[:-1], cu[1:]):
+        for r in range(a, b - BLOCK + 1, BLOCK):
+            yield slice(r, b if b - r < 2 * BLOCK else r + BLOCK)
+
+
+def assert_block_norms(got, want, errors, cu, what=""):
+    for name, x, w, e in zip(("dQ", "dK", "dV"), got, want, errors):
+        for rows in blocks(cu):
+            err = (x[rows].double() - w[rows]).square().sum((0, 2)).sqrt()
+            over = (err / e[rows].square().sum(0).sqrt()).max().item()
+            assert over <= 3.0, f"{what}: {name}, rows {rows.start} to {rows.stop}: {over:.2f} times its error"  # (NaN fails too)
