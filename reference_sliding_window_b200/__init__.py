@@ -554,9 +554,9 @@ class Rotary:
 
     def __call__(self, Q: torch.Tensor, K: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
                  first: int = 0):
-        """apply as a differentiable function of Q and K."""
+        """apply as a differentiable function of Q and K (any number of times)."""
         _check_capture(*((Q,) if K is None else (Q, K)))
-        r = _Turn.apply(self, positions, first, *((Q,) if K is None else (Q, K)))
+        r = _Turn.apply(self, positions, first, False, *((Q,) if K is None else (Q, K)))
         return r[0] if K is None else r
 
     def _stride(self, name: str, t: torch.Tensor, rows: int, like: torch.Tensor, index: int) -> int:
@@ -669,47 +669,75 @@ def _grad(t: torch.Tensor) -> torch.Tensor:
 
 class _Turn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rotary, positions, first, Q, K=None):
-        ctx.rotary, ctx.first = rotary, first
+    def forward(ctx, rotary, positions, first, inverse, Q, K=None):
+        ctx.rotary, ctx.first, ctx.inverse = rotary, first, inverse
         ctx.save_for_backward(positions)
-        r = rotary.apply(Q, K, positions=positions, first=first)
+        r = rotary.apply(Q, K, positions=positions, first=first, inverse=inverse)
         return (r,) if K is None else r
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dQ, dK=None):
         positions, = ctx.saved_tensors
         g = (_grad(dQ),) if dK is None else (_grad(dQ), _grad(dK))
-        r = ctx.rotary.apply(*g, positions=positions, first=ctx.first, inverse=True)
-        return (None, None, None) + ((r,) if dK is None else r)
+        if torch.is_grad_enabled():  # create_graph: a turn is linear, and so is its gradient
+            r = _Turn.apply(ctx.rotary, positions, ctx.first, not ctx.inverse, *g)
+        else:
+            r = ctx.rotary.apply(*g, positions=positions, first=ctx.first, inverse=not ctx.inverse)
+            r = (r,) if dK is None else r
+        return (None, None, None, None) + r
+
+
+class _Once(torch.autograd.Function):
+    """The first n tensors as they are, as functions of the others that cannot be
+    differentiated.  (once_differentiable cuts the graph instead: a gradient of
+    something that holds both an output and its gradient would then lack the
+    second part, without a word.)"""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.view_as(t) for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("masked_attention is once differentiable: its gradients (create_graph=True) have none")
 
 
 class _MaskedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, V, cu_seqlens, ref_lens, n, scale, bidir_prefix, rotary, positions):
+        graph = ()
         if rotary is not None:
+            # What is saved of Q and K is their turned copies; an empty piece
+            # of each keeps the gradients' dependence on them (and no memory).
+            with torch.enable_grad():
+                graph = tuple(t[:0].clone() for t in (Q, K) if t.requires_grad)
             Q, K = rotary.apply(Q, K, positions=positions)
         O, lse = _forward_lse(Q, K, V, cu_seqlens, ref_lens, n, scale, None, bidir_prefix)
-        ctx.save_for_backward(Q, K, V, O, lse, positions)
+        ctx.save_for_backward(Q, K, V, O, lse, positions, *graph)
         ctx.args = (cu_seqlens, ref_lens, n, scale, None, bidir_prefix)
         ctx.rotary = rotary
         return O
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
-        Q, K, V, O, lse, positions = ctx.saved_tensors
-        dQ, dK, dV = masked_backward_varlen(_grad(dO), Q, K, V, O, lse, *ctx.args)
-        if ctx.rotary is not None:
-            ctx.rotary.apply(dQ, dK, positions=positions, inverse=True, out=(dQ, dK))
-        return (dQ, dK, dV) + (None,) * 7
+        Q, K, V, O, lse, positions, *graph = ctx.saved_tensors
+        with torch.no_grad():
+            grads = masked_backward_varlen(_grad(dO), Q, K, V, O, lse, *ctx.args)
+            if ctx.rotary is not None:
+                ctx.rotary.apply(*grads[:2], positions=positions, inverse=True, out=grads[:2])
+        if torch.is_grad_enabled():  # create_graph
+            of = [t for t in (dO, Q, K, V, *graph) if t.requires_grad]
+            if of:
+                grads = _Once.apply(3, *grads, *of)
+        return grads + (None,) * 7
 
 
 def masked_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, L_m: int, n: int, scale: float = 0.0,
                      bidir_prefix: bool = False, rotary: Optional[Rotary] = None,
                      positions: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """masked_forward as a differentiable function of Q, K and V (once
-    differentiable).  rotary: Q and K are turned first, to positions (int32
+    """masked_forward as a differentiable function of Q, K and V, once: a
+    second derivative raises, and so do forward mode and torch.func's
+    transforms.  rotary: Q and K are turned first, to positions (int32
     [L] on the device; None: 0 .. L-1), and their gradients turned back."""
     if rotary is None and positions is not None:
         raise ValueError("positions without rotary")
