@@ -272,6 +272,7 @@ rswa_status rswa_masked_forward_ex(const void* Q, const void* K, const void* V, 
  *     increasing (every document has at least one row).
  *   ref_lens: HOST int32[n_docs], 0 <= ref_lens[i] <= length of document i.
  *   n_docs >= 1; n, H, d, dtype, scale, flags as in rswa_masked_forward_ex.
+ * An infinity or a NaN in one document leaves the others' rows as they are.
  * Every argument is checked before anything is enqueued.  BF16 with d = 128
  * runs the whole pack in one tensor-core launch (one CTA per document, pair
  * of 128-row query tiles and head, longest first; more than 1024 pairs are

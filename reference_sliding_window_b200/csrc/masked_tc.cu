@@ -233,6 +233,24 @@ __device__ __forceinline__ float half_exp(const float* s, int col0, int ra, int 
   }
 }
 
+// V rows past the document's end (rows [row0, 128) of the stage at `tile`) are the
+// next one's.  Their weights are 0, but 0 times an infinity is NaN: cleared once
+// the tile has landed and before the group's PV reads it.  (Both groups clear the
+// same rows; the stage is filled again only after both have handed P over.)  Out of
+// line: one tile of a document needs it, and the loop keeps its registers.
+__device__ __noinline__ bool clear_rows(uint32_t tile, int row0, uint32_t full, uint32_t parity, int r) {
+  const bool ok = mbar_wait_bounded(full, parity);
+  for (int c = r; c < (kTile - row0) * 16; c += kTile) {
+    const int row = row0 + c / 16, chunk = c % 16;
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                     tile + (chunk >> 3) * kBoxBytes + row * 128 + (chunk & 7) * 16),
+                 "r"(0)
+                 : "memory");
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  return ok;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) masked_tc_kernel(const __grid_constant__ TcParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -541,6 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) masked_tc_kernel(const __grid_con
       if (stamp) TC_CYC(j, 4);
       l_sum = l_sum * corr + lt;
       m_ref = m_new;
+      if (k0 + kTile > L &&
+          !clear_rows(sbase + kSmV + (j % kVS) * kTileBytes, L - k0, B(kBarVFull + j % kVS), (j / kVS) & 1, r))
+        ok = false;
       tc_fence_before();
       mbar_arrive(B(kBarPFull + g));
     }

@@ -101,3 +101,42 @@ def test_varlen_pack_with_short_documents_on_tensor_cores():
     torch.cuda.synchronize()
     want = oracle.masked_forward_varlen(Q.double().numpy(), K.double().numpy(), V.double().numpy(), cu, refs, n)
     assert_close(O, want, "bf16", "pack with short documents")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("cu,refs,n,bidir", [
+    ([0, 200, 330, 475], [60, 130, 10], 16, False),
+    ([0, 128, 130, 500, 501, 640], [100, 1, 300, 0, 139], 40, True),
+    ([0, 300, 700, 1000, 1001], [300, 400, 0, 1], 128, False),
+])
+def test_a_document_s_infinities_and_nan_stay_in_it(cu, refs, n, bidir, bad, dtype, d):
+    """Every second document's rows are bad: the others' outputs and log-sum-exps keep their bits."""
+    Q, K, V = (t.cuda() for t in synth.prefill_case(cu[-1], 2, d, dtype, seed=cu[-1]))
+    want = masked_forward_varlen(Q, K, V, cu, refs, n, bidir_prefix=bidir, return_lse=True)
+    for first in (0, 1):
+        q, k, v = (t.clone() for t in (Q, K, V))
+        clean = torch.ones(cu[-1], dtype=torch.bool, device="cuda")
+        for i in range(first, len(refs), 2):
+            clean[cu[i]:cu[i + 1]] = False
+        for t in (q, k, v):
+            t[~clean] = bad
+        O, lse = masked_forward_varlen(q, k, v, cu, refs, n, bidir_prefix=bidir, return_lse=True)
+        assert torch.equal(O[clean], want[0][clean]) and torch.equal(lse[:, clean], want[1][:, clean])
+        assert torch.equal(O[clean], masked_forward_varlen(q, k, v, cu, refs, n, bidir_prefix=bidir)[clean])
+
+
+def test_short_documents_from_memory_stay_apart():
+    """Thousands of documents shorter than a tile, more than L2 holds, NaN in every second one."""
+    H, d, docs, n = 10, 128, 1200, 40
+    rng = np.random.default_rng(4)
+    sizes = rng.integers(1, 128, size=docs)
+    cu = [0] + np.cumsum(sizes).tolist()
+    refs = [int(rng.integers(0, s + 1)) for s in sizes]
+    g = torch.Generator(device="cuda").manual_seed(4)
+    Q, K, V = (torch.randn((cu[-1], H, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    want = masked_forward_varlen(Q, K, V, cu, refs, n)
+    clean = torch.from_numpy(np.repeat(np.arange(docs) % 2 == 0, sizes)).cuda()
+    V[~clean] = float("nan")
+    for _ in range(3):
+        assert torch.equal(masked_forward_varlen(Q, K, V, cu, refs, n)[clean], want[clean])
