@@ -533,3 +533,36 @@ def test_refusals():
         masked_backward(dO, Q, K, V, O, lse, L_m=4, n=0)
     with pytest.raises(ValueError):
         masked_backward_varlen(dO, Q, K, V, O, lse, [0, 8, 15], [1, 1], 2)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("f32", 64)])
+def test_the_largest_tensors(dtype, d):
+    """Just under 2^31 elements a tensor: the last document of the pack has the
+    bits that it has alone."""
+    H, last = 16, 700
+    L = (2 ** 31 // d - 1) // H
+    if dtype == "f32":
+        L //= 4  # (8 tensors of 8.6 GB would do, but take their time)
+    cu, refs, n = [0, 100, L - last, L], [50, 0, 288], 128
+    g = torch.Generator(device="cuda").manual_seed(1)
+    t = [torch.empty((L, H, d), dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda") for _ in range(4)]
+    for x in t:
+        for rows in x.split(1 << 18):
+            rows.normal_(generator=g)
+    dO, Q, K, V = t
+    rot = Rotary(d)
+    Q, K = rot.apply(Q, K, out=(Q, K))
+    O, lse = masked_forward_varlen(Q, K, V, cu, refs, n, return_lse=True)
+    got = masked_backward_varlen(dO, Q, K, V, O, lse, cu, refs, n)
+    for a, b, ref in ((L - last, L, 288), (0, 100, 50)):
+        part = [x[a:b].clone() for x in (dO, Q, K, V, O)]
+        alone = masked_forward(*part[1:4], L_m=ref, n=n, return_lse=True)
+        assert torch.equal(part[4], alone[0]) and torch.equal(lse[:, a:b], alone[1])
+        want = masked_backward(*part, alone[1], L_m=ref, n=n)
+        for x, y in zip(got, want):
+            assert torch.equal(x[a:b], y)
+    # rows of the long window, against its own last rows run alone: dQ alone is whole there
+    a, b = L - last - 1280, L - last
+    part = [x[a:b].clone() for x in (dO, Q, K, V, O)]
+    want = masked_backward(*part, lse[:, a:b].contiguous(), L_m=0, n=n)
+    assert (got[0][a + n:b].float() - want[0][n:].float()).abs().max() <= 2.0 ** -6 * want[0].float().abs().max()
