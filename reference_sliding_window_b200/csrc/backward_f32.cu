@@ -8,7 +8,7 @@
 // dropped lo lo 2^-22 |x y|: a product is off by at most 1.25 2^-20, a few
 // float32 roundings.  Plain FMAs are bound by shared memory, not by the FMA
 // pipes: the register file takes 128 bytes a cycle from it, half of what 4x4
-// blocks a thread need (2011 rows, 10 heads, d = 128: 925 us, this kernel 605).
+// blocks a thread need (2011 rows, 10 heads, d = 128: 925 us, this kernel 598).
 // The tensor pipe is busy 53 % of that time (its rate for these MMAs, 1024
 // operations a cycle and SM, measured); loading the next tiles under this pair's
 // work saved under 1 %, so they are loaded plainly.

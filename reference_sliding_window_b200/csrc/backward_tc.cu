@@ -7,9 +7,10 @@
 // products per tile pair in a dK, dV item, 3 in a dQ item) and the operands it
 // reads from shared memory, with the exponentials close behind.  Measured at
 // 12832 + 19936 rows, 10 heads, d = 128: 3320 cycles a tile pair in dK, dV
-// items and 2440 in dQ items, of 2048 and 1536 at the MMA's rate; 5.0 ms, 875
-// TFLOP/s of the five products that the gradient cannot do without (5.6 ms,
-// 780 TFLOP/s, once the power limit has lowered the clock).
+// items and 2440 in dQ items, of 2048 and 1536 at the MMA's rate; 5.5 to 5.8 ms
+// in a stream of calls, whose clock the power limit lowers (4.9 to 5.3 ms for the
+// first ones): 750 to 790 TFLOP/s of the five products that the gradient cannot
+// do without.
 //
 // * A dK, dV item keeps its K and V tiles in shared memory and streams Q and
 //   dO tiles.  S and dP are formed transposed (keys on TMEM lanes), so that P
