@@ -221,3 +221,19 @@ def test_refusals():
         a.rotate(rot, x, x.clone())
     with pytest.raises(RSWAError, match="ARG"):
         a.rotate(Rotary(128), x, x.clone())
+
+
+@pytest.mark.parametrize("dim,interleaved", [(2, False), (6, True)])
+def test_more_than_2_32_threads(dim, interleaved):
+    """Element by element (rotary dims below a vector), in place, over a tensor of
+    9 10^9 elements: the rows have the values that they have in a small call."""
+    rows = 140_000_003
+    rot = Rotary(64, rotary_dim=dim, interleaved=interleaved)
+    Q = torch.empty((rows, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for part in Q.split(1 << 24):
+        part.normal_(generator=torch.Generator(device="cuda").manual_seed(part.storage_offset() & 0xffff))
+    some = [(0, 300), (rows // 2, rows // 2 + 300), ((1 << 27) - 150, (1 << 27) + 150), (rows - 300, rows)]
+    want = [rot.apply(Q[a:b].clone(), first=a) for a, b in some]
+    rot.apply(Q, out=Q)
+    for (a, b), w in zip(some, want):
+        assert torch.equal(Q[a:b], w)
